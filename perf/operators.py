@@ -104,10 +104,10 @@ def _gen(seed):
 
 
 def _pow2_scale(amax):
-    """The smallest power of two s >= 2^-100 with amax <= 448 s."""
+    """The smallest power of two s >= 2^-60 with amax <= 448 s, at most 2^30."""
     m, e = torch.frexp(amax)
     k = torch.where(m <= 0.875, e - 9, e - 8)
-    k = torch.where(amax > 0, k, torch.full_like(k, -100)).clamp(min=-100)
+    k = torch.where(amax > 0, k, torch.full_like(k, -60)).clamp(-60, 30)
     return torch.ldexp(torch.ones_like(amax), k)
 
 
@@ -420,7 +420,7 @@ def _exact_append(s):
                     cache[pg, :, o:o + end - at] = rows
                 else:
                     big = rows.abs().amax((1, 2))
-                    k = torch.ceil(torch.log2((big / 448.0).clamp(min=2.0 ** -100)))
+                    k = torch.ceil(torch.log2((big / 448.0).clamp(2.0 ** -60, 2.0 ** 30)))
                     now = torch.exp2(k)
                     if o:
                         now = torch.maximum(now, scale[pg])
