@@ -17,10 +17,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # kernels with device-side index checks); it is never a fallback
 LIB_PATH = os.path.join(_HERE, "libsamba_debug.so" if os.environ.get("SAMBA_LIBRARY") == "debug" else "libsamba.so")
 
-SAMBA_F32, SAMBA_BF16 = 0, 1
+SAMBA_F32, SAMBA_BF16, SAMBA_E4M3 = 0, 1, 2
 SAMBA_OK = 0
 SAMBA_ERR_INVALID_ARG, SAMBA_ERR_UNSUPPORTED, SAMBA_ERR_WORKSPACE = -1, -2, -3
-SAMBA_ERR_CUDA, SAMBA_ERR_TIMEOUT, SAMBA_ERR_CHECK = -4, -5, -6
+SAMBA_ERR_CUDA, SAMBA_ERR_TIMEOUT, SAMBA_ERR_CHECK, SAMBA_ERR_BATCH = -4, -5, -6, -7
 SCAN_FUSE_CONV, SCAN_DELTA_SOFTPLUS, SCAN_CONV_SILU = 1, 2, 4
 
 _vp = ctypes.c_void_p
@@ -78,6 +78,42 @@ class GemmArgs(ctypes.Structure):
                 ("out", GemmOut * 3), ("nout", _i32), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class PagedKvArgs(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64), ("page_size", _i32),
+                ("heads_kv", _i32), ("head_dim", _i32), ("dtype", _i32)]
+
+
+class PagedBatchArgs(ctypes.Structure):
+    _fields_ = [("q_start", _vp), ("kv_len", _vp), ("block_table", _vp), ("batch", _i64), ("rows", _i64),
+                ("max_pages", _i64), ("max_q", _i64), ("max_kv", _i64)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("freqs", _vp), ("ldq", _i64), ("ldk", _i64),
+                ("ldv", _i64), ("heads_q", _i32), ("rot_dim", _i32), ("interleaved", _i32), ("kv", PagedKvArgs),
+                ("batch", PagedBatchArgs)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("o", _vp), ("heads_q", _i32), ("scale", ctypes.c_float), ("window", _i64),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("kv", PagedKvArgs),
+                ("batch", PagedBatchArgs)]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("r", _vp), ("y", _vp), ("w_pre", _vp), ("w_post", _vp), ("gate", _vp), ("alpha", _vp),
+                ("r_out", _vp), ("n", _vp), ("rstd_pre", _vp), ("rstd_post", _vp), ("rows", _i64), ("width", _i64),
+                ("r_dtype", _i32), ("y_dtype", _i32), ("eps", ctypes.c_float)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [("dn", _vp), ("dr_out", _vp), ("r", _vp), ("w_pre", _vp), ("rstd_pre", _vp), ("y", _vp),
+                ("w_post", _vp), ("rstd_post", _vp), ("gate", _vp), ("alpha", _vp), ("dr", _vp), ("dy", _vp),
+                ("dgate", _vp), ("dw_pre", _vp), ("dw_post", _vp), ("dalpha", _vp), ("workspace", _vp),
+                ("workspace_bytes", ctypes.c_size_t), ("rows", _i64), ("width", _i64), ("r_dtype", _i32),
+                ("y_dtype", _i32)]
+
+
 class SambaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"samba error {code}: {msg}")
@@ -128,10 +164,19 @@ def load() -> ctypes.CDLL:
     lib.samba_swa_bwd.argtypes = [ctypes.POINTER(SwaBwdArgs), _vp]
     lib.samba_mixer_bwd.argtypes = [ctypes.POINTER(ScanBwdArgs), ctypes.POINTER(SwaBwdArgs), _vp, _vp]
     lib.samba_conv_state.argtypes = [_vp, ctypes.c_int, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, _vp]
+    lib.samba_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _vp]
+    lib.samba_paged_attn_workspace_size.argtypes = [ctypes.POINTER(PagedAttnArgs)]
+    lib.samba_paged_attn_workspace_size.restype = ctypes.c_size_t
+    lib.samba_paged_attn.argtypes = [ctypes.POINTER(PagedAttnArgs), _vp]
+    lib.samba_block_norm_fwd.argtypes = [ctypes.POINTER(BlockNormArgs), _vp]
+    lib.samba_block_norm_bwd_workspace_size.argtypes = [_i64, _i64]
+    lib.samba_block_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.samba_block_norm_bwd.argtypes = [ctypes.POINTER(BlockNormBwdArgs), _vp]
     for name in ("samba_conv1d_fwd", "samba_selective_scan_fwd", "samba_swa_fwd", "samba_mixer_prefill",
                  "samba_scan_step", "samba_swa_ring_fill", "samba_swa_step", "samba_get_status",
                  "samba_scan_carry", "samba_conv_state", "samba_gemm", "samba_selective_scan_bwd", "samba_swa_bwd",
-                 "samba_selftest_wait_timeout", "samba_swa_step_noalloc", "samba_selftest_check", "samba_mixer_bwd"):
+                 "samba_selftest_wait_timeout", "samba_swa_step_noalloc", "samba_selftest_check", "samba_mixer_bwd",
+                 "samba_kv_append", "samba_paged_attn", "samba_block_norm_fwd", "samba_block_norm_bwd"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

@@ -91,12 +91,14 @@ const char* samba_last_error(void) { return g_last_error.c_str(); }
 
 int samba_get_status(samba_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int codes[5] = {take_status_scan(s), take_status_swa(s), take_status_misc(s), take_status_gemm(s),
-                  take_status_swa_bwd(s)};
+  int codes[8] = {take_status_scan(s),    take_status_swa(s),       take_status_misc(s),       take_status_gemm(s),
+                  take_status_swa_bwd(s), take_status_kv_append(s), take_status_paged_attn(s), take_status_block_norm(s)};
   for (int c : codes)
     if (c == SAMBA_ERR_CUDA) return fail(SAMBA_ERR_CUDA, "samba_get_status: %s", cudaGetErrorString(cudaGetLastError()));
   for (int c : codes)
-    if (c != 0) return fail(c, "a kernel gave up a device-side wait");
+    if (c != 0)
+      return fail(c, c == SAMBA_ERR_BATCH ? "a paged batch description was out of range"
+                                          : "a kernel gave up a device-side wait");
   return SAMBA_OK;
 }
 
@@ -484,6 +486,143 @@ int samba_swa_step_noalloc(const void* q_t, const void* k_t, const void* v_t, vo
   if (!(scale > 0.f)) scale = 1.0f / std::sqrt(static_cast<float>(head_dim));
   return launch_swa_step_noalloc(q_t, k_t, v_t, k_ring, v_ring, pos, o_t, batch, heads_q, heads_kv, head_dim, window,
                                  scale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What every paged call checks: the pool, the batch description and the limits.
+static int check_paged(const samba_paged_kv& kv, const samba_paged_batch& bt, const char* who, bool pointers) {
+  if (kv.num_pages < 1 || kv.heads_kv < 1 || bt.batch < 0 || bt.rows < 0 || bt.max_pages < 0 || bt.max_q < 0 ||
+      bt.max_kv < 0)
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: bad shape", who);
+  if (kv.dtype != SAMBA_BF16 && kv.dtype != SAMBA_E4M3)
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: the cache must be SAMBA_BF16 or SAMBA_E4M3", who);
+  const int P = kv.page_size, d = kv.head_dim;
+  if (P != 16 && P != 32 && P != 64 && P != 128 && P != 256)
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64, 128 or 256", who);
+  if (d != 16 && d != 32 && d != 64 && d != 128)
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: head_dim must be 16, 32, 64 or 128", who);
+  if (kv.heads_kv > 65535 || bt.batch > 65535) return fail(SAMBA_ERR_UNSUPPORTED, "%s: batch or heads_kv above 65535", who);
+  if (kv.num_pages > INT32_MAX / kv.heads_kv)
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: num_pages * heads_kv must be below 2^31", who);
+  const int64_t lim = int64_t(1) << 30;
+  if (bt.rows >= lim || bt.max_q >= lim || bt.max_kv >= lim || bt.max_pages >= lim)
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: rows, max_q, max_kv and max_pages must be below 2^30", who);
+  if (!pointers) return SAMBA_OK;
+  if (!kv.k || !kv.v) return fail(SAMBA_ERR_INVALID_ARG, "%s: the cache's k and v are required", who);
+  if ((kv.dtype == SAMBA_E4M3) != (kv.k_scale != nullptr) || (kv.dtype == SAMBA_E4M3) != (kv.v_scale != nullptr))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: k_scale and v_scale go with SAMBA_E4M3, and only with it", who);
+  if (bt.batch > 0 && (!bt.q_start || !bt.kv_len || (!bt.block_table && bt.max_pages > 0)))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: q_start, kv_len and block_table are required", who);
+  if (!aligned16(kv.k) || !aligned16(kv.v)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned cache", who);
+  return SAMBA_OK;
+}
+
+int samba_kv_append(const samba_kv_append_args* a, samba_stream_t stream) {
+  const char* who = "samba_kv_append";
+  if (!a) return fail(SAMBA_ERR_INVALID_ARG, "%s: null args", who);
+  const int rc = check_paged(a->kv, a->batch, who, true);
+  if (rc != SAMBA_OK) return rc;
+  const int64_t d = a->kv.head_dim, nk = a->kv.heads_kv * d;
+  if (!a->k || !a->v) return fail(SAMBA_ERR_INVALID_ARG, "%s: k and v are required", who);
+  if ((a->q != nullptr) != (a->q_out != nullptr)) return fail(SAMBA_ERR_INVALID_ARG, "%s: q and q_out go together", who);
+  if (a->q && (a->heads_q < 1 || a->heads_q > 65535)) return fail(SAMBA_ERR_INVALID_ARG, "%s: bad heads_q", who);
+  if (a->ldk < nk || a->ldv < nk || a->ldk % 8 || a->ldv % 8 || (a->q && (a->ldq < a->heads_q * d || a->ldq % 8)))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: row strides must hold a row and be multiples of 8", who);
+  if (a->rot_dim < 0 || a->rot_dim > d || a->rot_dim % 16 || (a->rot_dim > 0) != (a->freqs != nullptr))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: rot_dim must be a multiple of 16 up to head_dim, with freqs unless it is 0", who);
+  if (a->q == a->q_out && a->q && a->ldq != a->heads_q * d)
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: q_out may be q only if q is contiguous", who);
+  const void* ptrs[] = {a->q, a->k, a->v, a->q_out};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  return launch_kv_append(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int check_paged_attn(const samba_paged_attn_args* a, const char* who, bool pointers) {
+  if (!a) return fail(SAMBA_ERR_INVALID_ARG, "%s: null args", who);
+  const int rc = check_paged(a->kv, a->batch, who, pointers);
+  if (rc != SAMBA_OK) return rc;
+  if (a->heads_q < 1 || a->heads_q % a->kv.heads_kv != 0)
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: heads_q must be a multiple of heads_kv", who);
+  if (a->heads_q / a->kv.heads_kv > 16) return fail(SAMBA_ERR_UNSUPPORTED, "%s: heads_q / heads_kv must be <= 16", who);
+  if (a->batch.max_q * a->heads_q >= (int64_t(1) << 30))
+    return fail(SAMBA_ERR_UNSUPPORTED, "%s: max_q * heads_q must be below 2^30", who);
+  if (a->window < 0) return fail(SAMBA_ERR_INVALID_ARG, "%s: negative window", who);
+  if (a->window >= (int64_t(1) << 30)) return fail(SAMBA_ERR_UNSUPPORTED, "%s: window must be below 2^30", who);
+  return SAMBA_OK;
+}
+
+size_t samba_paged_attn_workspace_size(const samba_paged_attn_args* a) {
+  if (check_paged_attn(a, "samba_paged_attn_workspace_size", false) != SAMBA_OK) return SIZE_MAX;
+  return paged_attn_workspace(*a);
+}
+
+int samba_paged_attn(const samba_paged_attn_args* a, samba_stream_t stream) {
+  const char* who = "samba_paged_attn";
+  const int rc = check_paged_attn(a, who, true);
+  if (rc != SAMBA_OK) return rc;
+  if (!a->q || !a->o) return fail(SAMBA_ERR_INVALID_ARG, "%s: q and o are required", who);
+  if (!aligned16(a->q) || !aligned16(a->o)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  const size_t need = paged_attn_workspace(*a);
+  if (need > 0 && (need == SIZE_MAX || !a->workspace || a->workspace_bytes < need))
+    return fail(SAMBA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need, a->workspace_bytes);
+  if (a->workspace && !aligned16(a->workspace)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned workspace", who);
+  return launch_paged_attn(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int check_norm_shape(int64_t rows, int64_t width, int r_dtype, int y_dtype, const char* who) {
+  if (rows < 0 || width < 8 || width % 8) return fail(SAMBA_ERR_INVALID_ARG, "%s: rows >= 0 and width a multiple of 8", who);
+  if (rows > INT32_MAX || width > 8192) return fail(SAMBA_ERR_UNSUPPORTED, "%s: width above 8192 or too many rows", who);
+  if (!dtype_ok(r_dtype) || !dtype_ok(y_dtype)) return fail(SAMBA_ERR_UNSUPPORTED, "%s: dtype must be SAMBA_F32 or SAMBA_BF16", who);
+  return SAMBA_OK;
+}
+
+int samba_block_norm_fwd(const samba_block_norm_args* a, samba_stream_t stream) {
+  const char* who = "samba_block_norm_fwd";
+  if (!a) return fail(SAMBA_ERR_INVALID_ARG, "%s: null args", who);
+  const int rc = check_norm_shape(a->rows, a->width, a->r_dtype, a->y_dtype, who);
+  if (rc != SAMBA_OK) return rc;
+  if (!a->r || (a->n != nullptr) != (a->w_pre != nullptr) || (a->y != nullptr) != (a->r_out != nullptr) || (!a->y && !a->n))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: r is required, n goes with w_pre, r_out with y, and one of n and y is needed", who);
+  if (!a->y && (a->w_post || a->gate || a->alpha))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: w_post, gate and alpha go with y", who);
+  if ((a->rstd_pre && !a->n) || (a->rstd_post && !a->w_post))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: rstd_pre goes with n and rstd_post with w_post", who);
+  if (!(a->eps >= 0.f)) return fail(SAMBA_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  const void* ptrs[] = {a->r, a->y, a->w_pre, a->w_post, a->gate, a->alpha, a->r_out, a->n};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  return launch_block_norm_fwd(*a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t samba_block_norm_bwd_workspace_size(int64_t rows, int64_t width) {
+  if (rows < 1 || width < 1 || width > 8192) return 0;
+  return block_norm_bwd_workspace(rows, width);
+}
+
+int samba_block_norm_bwd(const samba_block_norm_bwd_args* a, samba_stream_t stream) {
+  const char* who = "samba_block_norm_bwd";
+  if (!a) return fail(SAMBA_ERR_INVALID_ARG, "%s: null args", who);
+  const int rc = check_norm_shape(a->rows, a->width, a->r_dtype, a->y_dtype, who);
+  if (rc != SAMBA_OK) return rc;
+  if ((!a->dn && !a->dr_out) || !a->dr) return fail(SAMBA_ERR_INVALID_ARG, "%s: dr and one of dn and dr_out are required", who);
+  if (a->dn && (!a->r || !a->w_pre || !a->rstd_pre || !a->dw_pre))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: dn needs r, w_pre, rstd_pre and dw_pre", who);
+  if ((a->y != nullptr) != (a->dy != nullptr) || (a->gate != nullptr) != (a->dgate != nullptr) ||
+      (a->alpha != nullptr) != (a->dalpha != nullptr) || (a->w_post != nullptr) != (a->dw_post != nullptr) ||
+      (a->w_post && !a->rstd_post) || (!a->dn && a->dw_pre))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: every input goes with its gradient (and w_post with rstd_post)", who);
+  if (!a->y && (a->w_post || a->gate || a->alpha))
+    return fail(SAMBA_ERR_INVALID_ARG, "%s: w_post, gate and alpha go with y", who);
+  const void* ptrs[] = {a->dn, a->dr_out, a->r, a->w_pre, a->y, a->w_post, a->gate, a->alpha, a->dr, a->dy, a->dgate,
+                        a->dw_pre, a->dw_post, a->dalpha, a->workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(SAMBA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (a->rows > 0) {
+    const size_t need = block_norm_bwd_workspace(a->rows, a->width);
+    if (!a->workspace || a->workspace_bytes < need)
+      return fail(SAMBA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
+  }
+  return launch_block_norm_bwd(*a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

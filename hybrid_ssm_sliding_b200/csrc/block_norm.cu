@@ -1,0 +1,591 @@
+// The norms around a block with its gate, residual scale and residual sum, and
+// their gradients.  Per row of C elements, rms(x) = x / sqrt(mean(x^2) + eps):
+//   t = rms(y) w_post,  r' = r + alpha sigmoid(gate) t,  n = rms(r') w_pre
+// Everything is elementwise but the row sums, so HBM bandwidth bounds both
+// directions: every tensor is read or written once.
+//
+// A block stays resident and walks over groups of rows (one row of 2048
+// elements and more, several shorter ones, about 256 threads).  A group's
+// tensors are contiguous, so one bulk copy each brings them into a ring of
+// shared memory stages: the next groups' bytes are in flight while this one
+// waits for its sums, at no cost in registers.  A call with no more groups
+// than blocks reads global memory directly, which saves the copy's latency.  A thread has two runs of four
+// elements, so that 16- and 32-bit tensors both move without a gap.
+//
+// The backward pass needs one joint sum a row: with c = alpha s w_post yh and
+// s1 = sum dn w_pre x, the second norm's sum is
+//   sum c g = sum c (dr' + rstd dn w_pre) - rstd s1 / C sum c x.
+// The column sums (dw_pre, dw_post, dalpha) stay in registers over all rows of
+// a block; each block writes them once and a second kernel adds the blocks in
+// a fixed order (no atomics, so results repeat bit for bit).
+#include <algorithm>
+
+#include "common.cuh"
+#include "host.hpp"
+#include "pdl.cuh"
+
+namespace samba {
+
+__device__ __forceinline__ void load4(float* f, const float* p) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void load4(float* f, const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// sigmoid(x); the fast divide gives 0 where 1 + exp(-x) passes 2^126
+__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// How a call is cut up: rows a group, threads a row (a multiple of 32), and
+// where a tensor lies in a stage.
+struct NormShape {
+  int64_t rows, groups;
+  int C, rpb, tpr, stages, stage_bytes, off[5];
+  float inv_c;
+};
+
+constexpr int kNormMaxStages = 4;
+
+// Shared memory: [barriers][sum slots][stages].
+struct NormShared {
+  uint64_t full[kNormMaxStages];
+  int abort_flag, pad[3];
+  float slots[2][32][4];
+};
+constexpr int kNormHead = (int)((sizeof(NormShared) + 127) / 128 * 128);
+
+// Sums of N values over the warps of a row, the same bits in every thread.
+// `ph` alternates between two slots, so one barrier per call is enough: a slot
+// is written again only after the barrier of the call in between.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], NormShared& sh, int& ph, int tpr) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  const int nw = tpr >> 5;
+  if (nw == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / nw * nw;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh.slots[ph][warp][i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lane < nw ? sh.slots[ph][w0 + lane][i] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  ph ^= 1;
+}
+
+// The ring over a call's input tensors.
+struct NormTensor {
+  const void* p;  // null: not part of the call
+  int elem;       // bytes an element
+};
+template <int NTEN>
+struct NormInputs {
+  NormTensor t[NTEN];
+};
+
+template <int NTEN>
+__device__ __forceinline__ void norm_issue(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
+                                           unsigned char* ring, int64_t group, int stage) {
+  const int64_t row0 = group * s.rpb;
+  const int n = static_cast<int>(s.rows - row0 < s.rpb ? s.rows - row0 : s.rpb) * s.C;
+  uint32_t bytes = 0;
+#pragma unroll
+  for (int i = 0; i < NTEN; ++i)
+    if (in.t[i].p) bytes += n * in.t[i].elem;
+  mbar_arrive_expect_tx(&sh.full[stage], bytes);
+#pragma unroll
+  for (int i = 0; i < NTEN; ++i)
+    if (in.t[i].p)
+      bulk_load(ring + stage * s.stage_bytes + s.off[i],
+                reinterpret_cast<const unsigned char*>(in.t[i].p) + row0 * s.C * in.t[i].elem, n * in.t[i].elem,
+                &sh.full[stage]);
+}
+
+// Walks over this block's groups: body(row, in, at) where `at(i)` is tensor
+// i's first element of the thread's row (in the ring or in global memory) and
+// read() has to run it before the stage is released.  READ loads a row's
+// values into registers; BODY computes with them.
+template <bool RING, int NTEN, class Read, class Body>
+__device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
+                                          unsigned char* ring, Read&& read, Body&& body) {
+  const int sub = threadIdx.x / s.tpr;
+  int64_t first = blockIdx.x;
+  if constexpr (RING) {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < s.stages && first + (int64_t)i * gridDim.x < s.groups; ++i)
+        norm_issue(in, s, sh, ring, first + (int64_t)i * gridDim.x, i);
+  }
+  int stage = 0, parity = 0;
+  for (int64_t g = first; g < s.groups; g += gridDim.x) {
+    const int64_t row = g * s.rpb + sub;
+    const bool live = row < s.rows;
+    if constexpr (RING) {
+      const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort_flag);
+      if (ok && live)
+        read(row, [&](int i) { return ring + stage * s.stage_bytes + s.off[i] + (int64_t)sub * s.C * in.t[i].elem; });
+      if (!__syncthreads_and(ok)) {  // a wait gave up: leave once the copies in flight have landed
+        if (threadIdx.x == 0) {
+          volatile int never = 0;
+          int64_t h = g + gridDim.x;
+          for (int i = 1; i < s.stages && h < s.groups; ++i, h += gridDim.x) {
+            const int st = (stage + i) % s.stages;
+            mbar_wait(&sh.full[st], parity ^ (stage + i >= s.stages ? 1 : 0), &never);
+          }
+        }
+        return;
+      }
+      if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
+        norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
+      if (++stage == s.stages) stage = 0, parity ^= 1;
+    } else if (live) {
+      read(row, [&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + row * s.C * in.t[i].elem; });
+    }
+    body(row, live);
+  }
+}
+
+template <bool RING>
+__device__ __forceinline__ void norm_setup(NormShared& sh, const NormShape& s) {
+  if constexpr (RING) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < s.stages; ++i) mbar_init(&sh.full[i], 1);
+      sh.abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+}
+
+struct NormFwdParams {
+  NormInputs<3> in;  // r, y, gate
+  const float* w_pre;
+  const float* w_post;
+  const float* alpha;
+  void* r_out;
+  void* n;
+  float* rstd_pre;
+  float* rstd_post;
+  NormShape s;
+  float eps;
+};
+
+// A vector's values for the thread's eight elements, 1 without one.
+__device__ __forceinline__ void load_vec(float (&f)[8], const float* w, const int (&e)[2], const bool (&has)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (w && has[k]) load4(f + 4 * k, w + e[k]);
+    else f[4 * k] = f[4 * k + 1] = f[4 * k + 2] = f[4 * k + 3] = 1.f;
+  }
+}
+
+template <typename RT, typename YT, int MAXT, bool RING>
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  NormShared& sh = *reinterpret_cast<NormShared*>(sm);
+  const NormShape& s = p.s;
+  const int lt = threadIdx.x % s.tpr;
+  const int e[2] = {4 * lt, 4 * (lt + s.tpr)};
+  const bool has[2] = {e[0] < s.C, e[1] < s.C};
+  const bool has_y = p.in.t[1].p != nullptr, has_g = p.in.t[2].p != nullptr;
+  norm_setup<RING>(sh, s);
+  float r[8], y[8], z[8];
+  int ph = 0;
+  norm_walk<RING>(
+      p.in, s, sh, sm + kNormHead,
+      [&](int64_t, auto at) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!has[k]) continue;
+          load4(r + 4 * k, reinterpret_cast<const RT*>(at(0)) + e[k]);
+          if (has_y) load4(y + 4 * k, reinterpret_cast<const YT*>(at(1)) + e[k]);
+          if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(2)) + e[k]);
+        }
+      },
+      [&](int64_t row, bool live) {
+        float sum[1];
+        if (has_y) {
+          float rs = 1.f;
+          if (p.w_post) {
+            sum[0] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (live && has[i / 4]) sum[0] = fmaf(y[i], y[i], sum[0]);
+            row_sum(sum, sh, ph, s.tpr);
+            rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
+            if (p.rstd_post && live && lt == 0) p.rstd_post[row] = rs;
+          }
+          float w[8], a[8];
+          load_vec(w, p.w_post, e, has);
+          load_vec(a, p.alpha, e, has);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float u = y[i] * rs * w[i] * a[i];
+            if (has_g) u *= sigmoidf(z[i]);
+            r[i] += u;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
+              store4(reinterpret_cast<RT*>(p.r_out) + row * s.C + e[k], r + 4 * k);
+        }
+        if (p.n) {
+          sum[0] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (live && has[i / 4]) sum[0] = fmaf(r[i], r[i], sum[0]);
+          row_sum(sum, sh, ph, s.tpr);
+          const float rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
+          if (p.rstd_pre && live && lt == 0) p.rstd_pre[row] = rs;
+          float w[8];
+          load_vec(w, p.w_pre, e, has);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] *= r[i] * rs;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
+              store4(reinterpret_cast<YT*>(p.n) + row * s.C + e[k], w + 4 * k);
+        }
+      });
+}
+
+struct NormBwdParams {
+  NormInputs<5> in;  // dn, r (with dn), dr_out, y, gate
+  const float* w_pre;
+  const float* rstd_pre;
+  const float* w_post;
+  const float* rstd_post;
+  const float* alpha;
+  void* dr;
+  void* dy;
+  void* dgate;
+  float* part;  // [3][grid][C]: column sums of dw_pre, dw_post, dalpha
+  NormShape s;
+};
+
+template <typename RT, typename YT, int MAXT, bool RING>
+__global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  NormShared& sh = *reinterpret_cast<NormShared*>(sm);
+  const NormShape& s = p.s;
+  const int lt = threadIdx.x % s.tpr, sub = threadIdx.x / s.tpr;
+  const int e[2] = {4 * lt, 4 * (lt + s.tpr)};
+  const bool has[2] = {e[0] < s.C, e[1] < s.C};
+  const bool has_n = p.in.t[0].p != nullptr, has_d = p.in.t[2].p != nullptr, has_y = p.in.t[3].p != nullptr,
+             has_g = p.in.t[4].p != nullptr;
+  norm_setup<RING>(sh, s);
+  float a_pre[8], a_post[8], a_al[8], dn[8], x[8], g[8], yh[8], z[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a_pre[i] = a_post[i] = a_al[i] = 0.f;
+  float rs = 0.f, rsy = 1.f, rs_next = 0.f, rsy_next = 1.f;
+  auto stats = [&](int64_t row) {  // a row's factors, read one group ahead
+    if (row >= s.rows) return;
+    if (has_n) rs_next = p.rstd_pre[row];
+    if (p.w_post) rsy_next = p.rstd_post[row];
+  };
+  stats((int64_t)blockIdx.x * s.rpb + sub);
+  int ph = 0;
+  norm_walk<RING>(
+      p.in, s, sh, sm + kNormHead,
+      [&](int64_t, auto at) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (!has[k]) continue;
+          if (has_n) {
+            load4(dn + 4 * k, reinterpret_cast<const YT*>(at(0)) + e[k]);
+            load4(x + 4 * k, reinterpret_cast<const RT*>(at(1)) + e[k]);
+          }
+          if (has_d) load4(g + 4 * k, reinterpret_cast<const RT*>(at(2)) + e[k]);
+          if (has_y) load4(yh + 4 * k, reinterpret_cast<const YT*>(at(3)) + e[k]);
+          if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(4)) + e[k]);
+        }
+      },
+      [&](int64_t row, bool live) {
+        rs = rs_next, rsy = rsy_next;
+        stats(row + (int64_t)gridDim.x * s.rpb);
+        if (!live) rs = 0.f, rsy = 0.f;
+        float w[8], c[8], sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool in = live && has[i / 4];
+          if (!in || !has_n) dn[i] = x[i] = 0.f;
+          if (!in || !has_d) g[i] = 0.f;
+          if (!in || !has_y) yh[i] = 0.f;
+          if (!in || !has_g) z[i] = 0.f;
+        }
+        if (has_n) {
+          load_vec(w, p.w_pre, e, has);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= rs;
+            a_pre[i] = fmaf(dn[i], x[i], a_pre[i]);
+            dn[i] *= w[i];
+            sum[0] = fmaf(dn[i], x[i], sum[0]);
+            g[i] = fmaf(rs, dn[i], g[i]);
+          }
+        }
+        float sg[8];
+        if (has_y) {
+          load_vec(w, p.w_post, e, has);
+          load_vec(c, p.alpha, e, has);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sg[i] = has_g ? sigmoidf(z[i]) : 1.f;
+            yh[i] *= rsy;
+          }
+          if (p.w_post) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float ci = c[i] * sg[i] * w[i] * yh[i];
+              sum[1] = fmaf(ci, g[i], sum[1]);
+              sum[2] = fmaf(ci, x[i], sum[2]);
+            }
+          }
+        }
+        if (has_n || p.w_post) row_sum(sum, sh, ph, s.tpr);
+        const float m1 = rs * sum[0] * s.inv_c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = fmaf(-m1, x[i], g[i]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
+            store4(reinterpret_cast<RT*>(p.dr) + row * s.C + e[k], g + 4 * k);
+        if (has_y) {
+          const float m2 = p.w_post ? fmaf(-m1, sum[2], sum[1]) * s.inv_c : 0.f;
+          float dz[8], dy[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float t = yh[i] * w[i], gs = g[i] * sg[i], dt = c[i] * gs;
+            a_al[i] = fmaf(gs, t, a_al[i]);
+            a_post[i] = fmaf(dt, yh[i], a_post[i]);
+            dz[i] = dt * t * (1.f - sg[i]);
+            dy[i] = rsy * (dt * w[i] - yh[i] * m2);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C)) {
+              store4(reinterpret_cast<YT*>(p.dy) + row * s.C + e[k], dy + 4 * k);
+              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + row * s.C + e[k], dz + 4 * k);
+            }
+        }
+      });
+  // this block's column sums: the row slots of a group added in order, then written once
+  const int64_t plane = (int64_t)gridDim.x * s.C;
+  float* mine = p.part + (int64_t)blockIdx.x * s.C;
+  float* acc = reinterpret_cast<float*>(sm + kNormHead);  // [rpb][C]
+  auto put = [&](const float (&a)[8], float* dst) {
+    if (s.rpb == 1) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (has[k]) store4(dst + e[k], a + 4 * k);
+      return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (has[k]) store4(acc + sub * s.C + e[k], a + 4 * k);
+    __syncthreads();
+    for (int i = 4 * threadIdx.x; i < s.C; i += 4 * blockDim.x) {
+      float f[4], h[4];
+      load4(f, acc + i);
+      for (int q = 1; q < s.rpb; ++q) {
+        load4(h, acc + q * s.C + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] += h[j];
+      }
+      store4(dst + i, f);
+    }
+  };
+  if (has_n) put(a_pre, mine);
+  if (p.w_post) put(a_post, mine + plane);
+  if (p.alpha) put(a_al, mine + 2 * plane);
+}
+
+// Adds the blocks' column sums: 8 threads x 4 columns by 32 slices of blocks,
+// the slices then added in order.
+__global__ void __launch_bounds__(256) block_norm_cols_kernel(const float* __restrict__ part, float* dw_pre,
+                                                              float* dw_post, float* dalpha, int nblk, int C) {
+  __shared__ float4 sums[32][8];
+  float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dalpha;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + 4 * tx;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (!out) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < C) {
+    const float* src = part + (int64_t)blockIdx.y * nblk * C + col;
+#pragma unroll 4
+    for (int b = ty; b < nblk; b += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)b * C);
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+  }
+  sums[ty][tx] = a;
+  __syncthreads();
+  if (ty == 0 && col < C && SAMBA_CHECK(col + 4 <= C)) {
+#pragma unroll 8
+    for (int s = 1; s < 32; ++s) {
+      const float4 v = sums[s][tx];
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+    *reinterpret_cast<float4*>(out + col) = a;
+  }
+}
+
+// ------------------------------------------------------------------ launchers
+// Threads an SM holds (forward 1024, at 64 registers; backward 512, whose
+// column sums take 24 more each); the stages then take the shared memory.
+constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
+constexpr int kNormSmem = 200 * 1024;
+
+struct NormCut {
+  NormShape s;
+  int grid, threads;
+  size_t smem;
+  bool ring;
+};
+
+static void norm_rows(int64_t C, int& tpr, int& rpb) {
+  tpr = static_cast<int>((C / 8 + 31) / 32 * 32);
+  rpb = std::max(1, 256 / tpr);
+}
+
+// Resident blocks by threads alone; a block's stage may take a whole SM, so
+// the shared memory then allows fewer.
+static int norm_blocks_per_sm(int64_t C, int threads_per_sm, int64_t stage_bytes) {
+  int tpr, rpb;
+  norm_rows(C, tpr, rpb);
+  const int by_threads = std::max(1, threads_per_sm / (tpr * rpb));
+  return std::max<int>(1, std::min<int64_t>(by_threads, kNormSmem / (stage_bytes + kNormHead)));
+}
+
+template <int NTEN>
+static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int threads_per_sm, bool colsums) {
+  NormCut c;
+  NormShape& s = c.s;
+  s.rows = rows;
+  s.C = (int)C;
+  norm_rows(C, s.tpr, s.rpb);
+  s.groups = (rows + s.rpb - 1) / s.rpb;
+  s.inv_c = 1.f / (float)C;
+  int64_t at = 0;
+  for (int i = 0; i < NTEN; ++i) {
+    s.off[i] = (int)at;
+    if (in.t[i].p) at += (int64_t)s.rpb * C * in.t[i].elem;
+  }
+  s.stage_bytes = (int)at;
+  const int per_sm = norm_blocks_per_sm(C, threads_per_sm, at);
+  const int64_t most = (int64_t)sm_count() * per_sm;
+  c.grid = (int)std::min(s.groups, most);
+  c.threads = s.tpr * s.rpb;
+  c.ring = s.groups > most;
+  s.stages = (int)std::min<int64_t>(kNormMaxStages, std::max<int64_t>(1, (kNormSmem / per_sm - kNormHead) / at));
+  c.smem = kNormHead + (c.ring ? (size_t)s.stages * s.stage_bytes : 0);
+  if (colsums && s.rpb > 1) c.smem = std::max(c.smem, kNormHead + (size_t)s.rpb * C * sizeof(float));
+  return c;
+}
+
+template <auto KERN, class P>
+static int norm_go(const NormCut& c, const P& p, cudaStream_t s, const char* who) {
+  static PerDeviceOnce attr;
+  const int rc = once_per_device(attr, [&] {
+    return cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) == cudaSuccess
+               ? SAMBA_OK
+               : fail(SAMBA_ERR_CUDA, "%s: cannot set shared memory size", who);
+  });
+  if (rc != SAMBA_OK) return rc;
+  const cudaError_t e = launch_pdl(KERN, dim3(c.grid), dim3(c.threads), c.smem, s, p);
+  if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+  return check_launch(who);
+}
+
+template <typename RT, typename YT>
+static int norm_fwd_t(const NormCut& c, const NormFwdParams& p, cudaStream_t s) {
+  const char* who = "samba_block_norm_fwd";
+  if (c.threads <= 512)
+    return c.ring ? norm_go<block_norm_fwd_kernel<RT, YT, 512, true>>(c, p, s, who)
+                  : norm_go<block_norm_fwd_kernel<RT, YT, 512, false>>(c, p, s, who);
+  return c.ring ? norm_go<block_norm_fwd_kernel<RT, YT, 1024, true>>(c, p, s, who)
+                : norm_go<block_norm_fwd_kernel<RT, YT, 1024, false>>(c, p, s, who);
+}
+
+template <typename RT, typename YT>
+static int norm_bwd_t(const NormCut& c, const NormBwdParams& p, cudaStream_t s) {
+  const char* who = "samba_block_norm_bwd";
+  if (c.threads <= 512)
+    return c.ring ? norm_go<block_norm_bwd_kernel<RT, YT, 512, true>>(c, p, s, who)
+                  : norm_go<block_norm_bwd_kernel<RT, YT, 512, false>>(c, p, s, who);
+  return c.ring ? norm_go<block_norm_bwd_kernel<RT, YT, 1024, true>>(c, p, s, who)
+                : norm_go<block_norm_bwd_kernel<RT, YT, 1024, false>>(c, p, s, who);
+}
+
+int launch_block_norm_fwd(const samba_block_norm_args& a, cudaStream_t s) {
+  if (a.rows == 0) return SAMBA_OK;
+  const bool rb = a.r_dtype == SAMBA_BF16, yb = a.y_dtype == SAMBA_BF16;
+  const int re = rb ? 2 : 4, ye = yb ? 2 : 4;
+  NormFwdParams p = {{{{a.r, re}, {a.y, ye}, {a.gate, ye}}}, a.w_pre, a.w_post, a.alpha, a.r_out, a.n, a.rstd_pre,
+                     a.rstd_post, {}, a.eps};
+  const NormCut c = norm_cut(p.in, a.rows, a.width, kFwdThreadsPerSm, false);
+  p.s = c.s;
+  if (rb && yb) return norm_fwd_t<__nv_bfloat16, __nv_bfloat16>(c, p, s);
+  if (rb) return norm_fwd_t<__nv_bfloat16, float>(c, p, s);
+  if (yb) return norm_fwd_t<float, __nv_bfloat16>(c, p, s);
+  return norm_fwd_t<float, float>(c, p, s);
+}
+
+size_t block_norm_bwd_workspace(int64_t rows, int64_t C) {
+  int tpr, rpb;
+  norm_rows(C, tpr, rpb);
+  const int64_t most = (int64_t)sm_count() * norm_blocks_per_sm(C, kBwdThreadsPerSm, 0);
+  return (size_t)std::min<int64_t>((rows + rpb - 1) / rpb, most) * 3 * (size_t)C * sizeof(float);
+}
+
+int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t s) {
+  const char* who = "samba_block_norm_bwd";
+  const int C = (int)a.width;
+  if (a.rows == 0) {  // no rows: the sums are empty
+    for (float* d : {a.dw_pre, a.dw_post, a.dalpha})
+      if (d && cudaMemsetAsync(d, 0, (size_t)C * sizeof(float), s) != cudaSuccess)
+        return fail(SAMBA_ERR_CUDA, "%s: memset failed", who);
+    return SAMBA_OK;
+  }
+  const bool rb = a.r_dtype == SAMBA_BF16, yb = a.y_dtype == SAMBA_BF16;
+  const int re = rb ? 2 : 4, ye = yb ? 2 : 4;
+  NormBwdParams p = {{{{a.dn, ye}, {a.dn ? a.r : nullptr, re}, {a.dr_out, re}, {a.y, ye}, {a.gate, ye}}},
+                     a.w_pre, a.rstd_pre, a.w_post, a.rstd_post, a.alpha, a.dr, a.dy, a.dgate,
+                     reinterpret_cast<float*>(a.workspace), {}};
+  const NormCut c = norm_cut(p.in, a.rows, a.width, kBwdThreadsPerSm, true);
+  p.s = c.s;
+  int rc;
+  if (rb && yb) rc = norm_bwd_t<__nv_bfloat16, __nv_bfloat16>(c, p, s);
+  else if (rb) rc = norm_bwd_t<__nv_bfloat16, float>(c, p, s);
+  else if (yb) rc = norm_bwd_t<float, __nv_bfloat16>(c, p, s);
+  else rc = norm_bwd_t<float, float>(c, p, s);
+  if (rc != SAMBA_OK || !(a.dn || a.w_post || a.alpha)) return rc;
+  const cudaError_t e = launch_pdl(block_norm_cols_kernel, dim3((C + 31) / 32, 3), dim3(256), 0, s, (const float*)p.part,
+                                   a.dn ? a.dw_pre : nullptr, a.dw_post, a.dalpha, c.grid, C);
+  if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+  return check_launch(who);
+}
+
+int take_status_block_norm(cudaStream_t s) { return take_status_word(s); }
+
+}  // namespace samba

@@ -90,5 +90,14 @@ int launch_swa_step_noalloc(const void* q_t, const void* k_t, const void* v_t, v
 int launch_swa_step(const void* q_t, const void* k_t, const void* v_t, void* k_ring, void* v_ring, int64_t* pos,
                     void* o_t, int64_t B, int Hq, int Hkv, int d, int64_t W, float scale, void* ws,
                     cudaStream_t stream);
+int launch_kv_append(const samba_kv_append_args& a, cudaStream_t stream);
+int take_status_kv_append(cudaStream_t s);
+size_t paged_attn_workspace(const samba_paged_attn_args& a);
+int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t stream);
+int take_status_paged_attn(cudaStream_t s);
+size_t block_norm_bwd_workspace(int64_t rows, int64_t C);
+int launch_block_norm_fwd(const samba_block_norm_args& a, cudaStream_t stream);
+int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t stream);
+int take_status_block_norm(cudaStream_t s);
 
 }  // namespace samba

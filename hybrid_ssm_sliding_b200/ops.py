@@ -7,6 +7,7 @@ device), and calls into libsamba.so on the current (or given) stream.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -39,7 +40,8 @@ def version() -> int:
 
 def get_status(stream=None) -> int:
     """Synchronises the stream and returns/clears the device status word
-    (SAMBA_OK or SAMBA_ERR_TIMEOUT)."""
+    (SAMBA_OK, SAMBA_ERR_TIMEOUT, or SAMBA_ERR_BATCH after a paged call whose
+    batch description was out of range)."""
     return L.load().samba_get_status(L.stream_handle(stream))
 
 
@@ -418,6 +420,315 @@ def swa_step(q_t, k_t, v_t, k_ring, v_ring, pos, window, scale=None, o_t=None, w
                                     L.ptr(o_t), Bsz, Hq, Hkv, d, window, float(scale) if scale else 0.0,
                                     L.ptr(workspace), workspace.numel(), L.stream_handle(stream)))
     return o_t
+
+
+# ------------------------------------------------------------- paged cache
+def _placed(named, stream):
+    """Checks that the tensors are on one device and the stream (if given) too;
+    returns a guard that makes the device current."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _lend(stream, *tensors):
+    """Memory allocated here for a call on another stream than the current one
+    is kept until that stream has passed the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+class PagedKv:
+    """A KV cache in pages (samba_paged_kv): k, v [num_pages, Hkv, page_size, d]
+    bf16, or e4m3 (torch.float8_e4m3fn) with k_scale, v_scale [num_pages, Hkv]
+    fp32, one power of two a page and kv head.  The tensors stay the caller's;
+    the object keeps them alive and its calls update them in place."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a [num_pages, Hkv, page_size, d] tensor")
+        codes = {torch.bfloat16: L.SAMBA_BF16, torch.float8_e4m3fn: L.SAMBA_E4M3}
+        if k.dtype not in codes:
+            raise TypeError(f"the cache must be bfloat16 or float8_e4m3fn, got {k.dtype}")
+        n, h, p, d = k.shape
+        if min(k.shape) < 1:
+            raise ValueError("the cache is empty")
+        _need(k, "k")
+        _need(v, "v", k.dtype, k.shape)
+        if (k.dtype == torch.float8_e4m3fn) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale go with an 8-bit cache, and only with it")
+        _opt(k_scale, "k_scale", torch.float32, (n, h))
+        _opt(v_scale, "v_scale", torch.float32, (n, h))
+        _placed((("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)), None)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.args = L.PagedKvArgs(L.ptr(k), L.ptr(v), L.ptr(k_scale), L.ptr(v_scale), n, p, h, d, codes[k.dtype])
+
+    @classmethod
+    def empty(cls, num_pages, heads_kv, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
+        """A zero-filled pool (8-bit: with scales of one)."""
+        shape = (num_pages, heads_kv, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=device).to(dtype) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        return cls(k, v, *(torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+class PagedBatch:
+    """Which rows of a call are which sequence's, and where its cache lies
+    (samba_paged_batch): q_start [B + 1], kv_len [B], block_table [B, max_pages]
+    int32 on the GPU, read there when a call runs.  max_q and max_kv are upper
+    bounds of a sequence's new rows and of its length with them."""
+
+    def __init__(self, q_start, kv_len, block_table, max_q, max_kv):
+        _need(kv_len, "kv_len", torch.int32)
+        if kv_len.dim() != 1:
+            raise ValueError("kv_len must be [B]")
+        B = kv_len.shape[0]
+        _need(q_start, "q_start", torch.int32, (B + 1,))
+        _need(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_pages]")
+        _placed((("q_start", q_start), ("kv_len", kv_len), ("block_table", block_table)), None)
+        self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
+        self.max_q, self.max_kv = int(max_q), int(max_kv)
+        if self.max_q < 0 or self.max_kv < 0:
+            raise ValueError("max_q and max_kv must not be negative")
+        self.args = L.PagedBatchArgs(L.ptr(q_start), L.ptr(kv_len), L.ptr(block_table), B, 0, block_table.shape[1],
+                                     self.max_q, self.max_kv)
+
+    def _with_rows(self, rows):
+        a = self.args
+        return L.PagedBatchArgs(a.q_start, a.kv_len, a.block_table, a.batch, rows, a.max_pages, a.max_q, a.max_kv)
+
+
+def _head_rows(t, name, heads, dim):
+    """Checks a [T, heads, dim] bf16 matrix of heads with any row stride; returns that stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape [rows, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    h = t.shape[1]
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} needs contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else h * dim
+
+
+def kv_append(q, k, v, cache, batch, freqs=None, interleaved=False, q_out=None, stream=None):
+    """Writes the batch's new keys and values k, v [T, Hkv, d] bf16 into the
+    paged cache, rotating keys and the queries q [T, Hq, d] (or None) by
+    position on the way (see samba_kv_append).  q, k and v may be column
+    ranges of one matrix (rows strided).  ``freqs`` [rot / 2] fp64: the angle
+    of a pair is position * freqs[j]; None: no rotation.  Returns the rotated
+    queries [T, Hq, d] (rows of no sequence are not written)."""
+    kv = cache.args
+    ldk = _head_rows(k, "k", kv.heads_kv, kv.head_dim)
+    ldv = _head_rows(v, "v", kv.heads_kv, kv.head_dim)
+    rows = k.shape[0]
+    if v.shape[0] != rows:
+        raise ValueError("k and v disagree on their rows")
+    ldq = heads_q = 0
+    if q is not None:
+        ldq = _head_rows(q, "q", None, kv.head_dim)
+        heads_q = q.shape[1]
+        if q.shape[0] != rows or heads_q < 1:
+            raise ValueError("q needs the rows of k and v, and a head")
+        if q_out is not None:
+            _need(q_out, "q_out", torch.bfloat16, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    rot = 0
+    if freqs is not None:
+        _need(freqs, "freqs", torch.float64)
+        rot = 2 * freqs.numel()
+        if freqs.dim() != 1 or rot < 1:
+            raise ValueError("freqs must be [rot / 2]")
+    named = (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("freqs", freqs), ("the cache", cache.k),
+             ("the batch", batch.kv_len))
+    with _placed(named, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            _lend(stream, q_out)
+        if rows == 0 or batch.args.batch == 0:
+            return q_out
+        a = L.KvAppendArgs(L.ptr(q), L.ptr(k), L.ptr(v), L.ptr(q_out), L.ptr(freqs), ldq, ldk, ldv, heads_q, rot,
+                           1 if interleaved else 0, kv, batch._with_rows(rows))
+        L.check(L.load().samba_kv_append(ctypes.byref(a), L.stream_handle(stream)))
+    return q_out
+
+
+def _paged_attn_struct(batch, cache, heads_q, window, rows=0, scale=None):
+    a = L.PagedAttnArgs()
+    a.heads_q, a.window, a.scale = int(heads_q), int(window), float(scale) if scale else 0.0
+    a.kv, a.batch = cache.args, batch._with_rows(rows)
+    return a
+
+
+def paged_attn_workspace_size(batch, cache, heads_q, window=0) -> int:
+    """Bytes of workspace of paged_attn for these bounds (0: none)."""
+    with _placed((("the cache", cache.k), ("the batch", batch.kv_len)), None):
+        n = L.load().samba_paged_attn_workspace_size(ctypes.byref(_paged_attn_struct(batch, cache, heads_q, window)))
+        if n == ctypes.c_size_t(-1).value:
+            raise L.SambaError(L.SAMBA_ERR_UNSUPPORTED, L.load().samba_last_error().decode() or "workspace too large")
+    return int(n)
+
+
+def paged_attn(q, cache, batch, window=0, scale=None, o=None, workspace=None, stream=None):
+    """Causal attention of the batch's rows q [T, Hq, d] bf16 over the paged
+    cache (which holds their keys and values already): the last ``window``
+    positions, or all with 0 (see samba_paged_attn).  Returns o (rows of no
+    sequence are not written)."""
+    kv = cache.args
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != kv.head_dim or q.shape[1] < 1:
+        raise ValueError(f"q must have shape [rows, heads, {kv.head_dim}], got {tuple(q.shape)}")
+    _opt(o, "o", torch.bfloat16, q.shape)
+    _opt(workspace, "workspace", torch.uint8)
+    with _placed((("q", q), ("the cache", cache.k), ("the batch", batch.kv_len), ("o", o), ("workspace", workspace)),
+                 stream):
+        lib = L.load()
+        a = _paged_attn_struct(batch, cache, q.shape[1], window, q.shape[0], scale)
+        if o is None:
+            o = torch.empty_like(q)
+            _lend(stream, o)
+        if q.shape[0] == 0 or batch.args.batch == 0:
+            return o
+        if workspace is None:
+            n = lib.samba_paged_attn_workspace_size(ctypes.byref(a))
+            if 0 < n < ctypes.c_size_t(-1).value:
+                workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+                _lend(stream, workspace)
+        a.q, a.o, a.workspace = L.ptr(q), L.ptr(o), L.ptr(workspace)
+        a.workspace_bytes = 0 if workspace is None else workspace.numel()
+        L.check(lib.samba_paged_attn(ctypes.byref(a), L.stream_handle(stream)))
+    return o
+
+
+# -------------------------------------------------------------- block norm
+def _norm_rows(r):
+    if not isinstance(r, torch.Tensor) or r.dim() < 1:
+        raise ValueError("r must be a [..., width] tensor")
+    C = r.shape[-1]
+    return r.numel() // C if C else 0, C
+
+
+def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, eps=1e-6, r_out=None, n=None,
+                   n_dtype=None, rstd_pre=None, rstd_post=None, stream=None):
+    """What stands between two blocks (see samba_block_norm_fwd), per row of
+    r [..., C] (bf16 or fp32): r' = r + alpha * sigmoid(gate) * rms(y) * w_post
+    and n = rms(r') * w_pre.  y and gate share a type (bf16 or fp32), which n
+    takes; without y (the norm before the first block) n takes ``n_dtype`` (r's by
+    default).  ``rstd_pre`` / ``rstd_post`` ([rows] fp32) receive the row
+    factors for block_norm_bwd.  Returns (r', n); n is None without w_pre, r'
+    is r without y."""
+    M, C = _norm_rows(r)
+    _need(r, "r")
+    L.dtype_code(r)
+    _opt(y, "y", None, r.shape)
+    ydt = y.dtype if y is not None else (n.dtype if n is not None else n_dtype or r.dtype)
+    if y is not None and n_dtype is not None and n_dtype != y.dtype:
+        raise TypeError("n has y's dtype")
+    _opt(gate, "gate", ydt, r.shape)
+    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (alpha, "alpha")):
+        _opt(t, name, torch.float32, (C,))
+    if w_pre is None and (n is not None or rstd_pre is not None):
+        raise ValueError("n and rstd_pre go with w_pre")
+    _opt(r_out, "r_out", r.dtype, r.shape)
+    _opt(n, "n", ydt, r.shape)
+    _opt(rstd_pre, "rstd_pre", torch.float32, (M,))
+    _opt(rstd_post, "rstd_post", torch.float32, (M,))
+    with _placed((("r", r), ("y", y), ("w_pre", w_pre), ("w_post", w_post), ("gate", gate), ("alpha", alpha),
+                  ("r_out", r_out), ("n", n), ("rstd_pre", rstd_pre), ("rstd_post", rstd_post)), stream):
+        if y is not None and r_out is None:
+            r_out = torch.empty_like(r)
+            _lend(stream, r_out)
+        if w_pre is not None and n is None:
+            n = torch.empty(r.shape, dtype=ydt, device=r.device)
+            _lend(stream, n)
+        a = L.BlockNormArgs(L.ptr(r), L.ptr(y), L.ptr(w_pre), L.ptr(w_post), L.ptr(gate), L.ptr(alpha), L.ptr(r_out),
+                            L.ptr(n), L.ptr(rstd_pre), L.ptr(rstd_post), M, C, L.dtype_code(r), _norm_code(ydt),
+                            float(eps))
+        if M > 0:
+            L.check(L.load().samba_block_norm_fwd(ctypes.byref(a), L.stream_handle(stream)))
+    return (r if y is None else r_out), n
+
+
+def _norm_code(dt):
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dt}")
+    return L.SAMBA_F32 if dt == torch.float32 else L.SAMBA_BF16
+
+
+def block_norm_bwd_workspace_size(rows, width) -> int:
+    return int(L.load().samba_block_norm_bwd_workspace_size(rows, width))
+
+
+def block_norm_bwd(dn, r, w_pre=None, rstd_pre=None, dr_out=None, y=None, w_post=None, rstd_post=None, gate=None,
+                   alpha=None, workspace=None, stream=None):
+    """Gradients of block_norm_fwd (see samba_block_norm_bwd) given dn = dL/dn
+    and dr_out = dL/dr' (either may be None): r is the forward's r', rstd_pre
+    and rstd_post its row factors.  Returns a dict with dr, dw_pre and, where
+    the forward input exists, dy, dw_post, dgate, dalpha."""
+    M, C = _norm_rows(r)
+    _need(r, "r")
+    rcode = L.dtype_code(r)
+    if dn is None and dr_out is None:
+        raise ValueError("one of dn and dr_out is needed")
+    if dn is not None and (w_pre is None or rstd_pre is None):
+        raise ValueError("dn needs w_pre and rstd_pre")
+    if y is None and (w_post is not None or gate is not None or alpha is not None):
+        raise ValueError("w_post, gate and alpha go with y")
+    if w_post is not None and rstd_post is None:
+        raise ValueError("w_post needs rstd_post")
+    ydt = y.dtype if y is not None else dn.dtype if dn is not None else r.dtype
+    _opt(dn, "dn", ydt, r.shape)
+    _opt(dr_out, "dr_out", r.dtype, r.shape)
+    _opt(y, "y", ydt, r.shape)
+    _opt(gate, "gate", ydt, r.shape)
+    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (alpha, "alpha")):
+        _opt(t, name, torch.float32, (C,))
+    _opt(rstd_pre, "rstd_pre", torch.float32, (M,))
+    _opt(rstd_post, "rstd_post", torch.float32, (M,))
+    _opt(workspace, "workspace", torch.uint8)
+    with _placed((("r", r), ("dn", dn), ("dr_out", dr_out), ("y", y), ("gate", gate), ("w_pre", w_pre),
+                  ("w_post", w_post), ("alpha", alpha), ("rstd_pre", rstd_pre), ("rstd_post", rstd_post),
+                  ("workspace", workspace)), stream):
+        def vec(on):
+            return torch.empty((C,), dtype=torch.float32, device=r.device) if on else None
+
+        out = {"dr": torch.empty_like(r), "dy": None if y is None else torch.empty_like(y),
+               "dgate": None if gate is None else torch.empty_like(gate), "dw_pre": vec(dn is not None),
+               "dw_post": vec(w_post is not None), "dalpha": vec(alpha is not None)}
+        if M == 0:
+            for key in ("dw_pre", "dw_post", "dalpha"):
+                if out[key] is not None:
+                    out[key].zero_()
+            return out
+        if workspace is None:
+            workspace = torch.empty((max(block_norm_bwd_workspace_size(M, C), 16),), dtype=torch.uint8, device=r.device)
+            _lend(stream, workspace)
+        _lend(stream, *out.values())
+        a = L.BlockNormBwdArgs(L.ptr(dn), L.ptr(dr_out), L.ptr(r), L.ptr(w_pre) if dn is not None else None,
+                               L.ptr(rstd_pre) if dn is not None else None, L.ptr(y), L.ptr(w_post),
+                               L.ptr(rstd_post) if w_post is not None else None, L.ptr(gate), L.ptr(alpha),
+                               L.ptr(out["dr"]), L.ptr(out["dy"]), L.ptr(out["dgate"]), L.ptr(out["dw_pre"]),
+                               L.ptr(out["dw_post"]), L.ptr(out["dalpha"]), L.ptr(workspace), workspace.numel(), M, C,
+                               rcode, _norm_code(ydt))
+        L.check(L.load().samba_block_norm_bwd(ctypes.byref(a), L.stream_handle(stream)))
+    return out
 
 
 def default_scale(head_dim: int) -> float:

@@ -38,6 +38,10 @@
  *    SAMBA_ERR_WORKSPACE (workspace too small), SAMBA_ERR_CUDA (a CUDA call
  *    or launch failed).  samba_last_error() gives a one-line description of
  *    the last failure on the calling host thread.
+ *  - The paged entry points take a device-side description of the batch (row
+ *    offsets, lengths, page numbers) that the host cannot check.  Their
+ *    kernels check it: a value out of range is skipped, never followed, and
+ *    SAMBA_ERR_BATCH is recorded in the status word.
  *  - Kernels never spin without a limit.  A device-side wait that runs out
  *    (which only a library bug can cause) stops the kernel cleanly and
  *    records SAMBA_ERR_TIMEOUT in a per-device status word that
@@ -57,7 +61,7 @@ extern "C" {
 typedef struct CUstream_st* samba_stream_t;
 
 /* element types */
-enum { SAMBA_F32 = 0, SAMBA_BF16 = 1 };
+enum { SAMBA_F32 = 0, SAMBA_BF16 = 1, SAMBA_E4M3 = 2 /* paged caches only */ };
 
 /* status codes */
 enum {
@@ -67,7 +71,8 @@ enum {
   SAMBA_ERR_WORKSPACE = -3,
   SAMBA_ERR_CUDA = -4,
   SAMBA_ERR_TIMEOUT = -5,
-  SAMBA_ERR_CHECK = -6          /* debug build only: a device-side index check failed */
+  SAMBA_ERR_CHECK = -6,         /* debug build only: a device-side index check failed */
+  SAMBA_ERR_BATCH = -7          /* a device-side batch description is out of range */
 };
 
 /* flags of samba_scan_args.flags */
@@ -85,8 +90,9 @@ const char* samba_last_error(void);
 
 /* Synchronises `stream`, then returns and clears this device's status word:
  * SAMBA_OK, or SAMBA_ERR_TIMEOUT if a kernel gave up a device-side wait since
- * the last call, or (debug build) SAMBA_ERR_CHECK if a device-side index
- * check failed.  Returns SAMBA_ERR_CUDA if the synchronisation itself fails.
+ * the last call, SAMBA_ERR_BATCH if a paged call's batch description was out
+ * of range, or (debug build) SAMBA_ERR_CHECK if a device-side index check
+ * failed.  Returns SAMBA_ERR_CUDA if the synchronisation itself fails.
  *
  * Debug build: libsamba_debug.so (hybrid_ssm_sliding_b200/build.py --debug)
  * is the same library compiled with SAMBA_DEBUG.  Its kernels check the
@@ -547,6 +553,210 @@ int samba_swa_step(const void* q_t, const void* k_t, const void* v_t, void* k_ri
 int samba_swa_step_noalloc(const void* q_t, const void* k_t, const void* v_t, void* k_ring, void* v_ring,
                            int64_t* pos, void* o_t, int64_t batch, int heads_q, int heads_kv, int head_dim,
                            int64_t window, float scale, samba_stream_t stream);
+
+/* ------------------------------------------------------------ paged cache
+ * A KV cache in pages, for batches of sequences of any lengths: the pool
+ * k, v [num_pages, Hkv, page_size, d] is shared by all sequences, and row b of
+ * block_table names the pages that hold positions 0.. of sequence b in order
+ * (position p lies in row p mod page_size of page block_table[b][p / page_size]).
+ *
+ * dtype SAMBA_BF16, or SAMBA_E4M3: 8-bit codes with one fp32 scale for each
+ * (page, kv head) in k_scale and v_scale [num_pages, Hkv]; the value of a code
+ * is code * scale.  Scales are powers of two between 2^-60 and 2^30 (what is
+ * stored may be 448 * 2^30 = 4.8e11 at most); any other scale reads as 2^-60.
+ * NaN is kept as NaN; magnitudes above 448 * scale (infinities, and what is
+ * past the largest scale) become 448 * scale.
+ *
+ * samba_paged_batch says which rows of a call belong to which sequence: rows
+ * q_start[b] .. q_start[b+1] - 1 are the n_b newest tokens of sequence b,
+ * whose length with them is kv_len[b], so row i of a sequence has position
+ * kv_len[b] - n_b + i.  n_b may be 0 (an idle sequence) and rows outside every sequence
+ * (padding) are left untouched.  max_q and max_kv are host-side upper bounds
+ * of n_b and kv_len[b]; they size the grid, so tight bounds are faster.
+ * All three arrays are read on the device, so a captured graph may be
+ * replayed after they were changed in place, within the bounds.
+ *
+ * Sequences are in the order of their rows (q_start does not decrease).
+ * The kernels check what they read: rows [q_start[b], q_start[b+1]) within
+ * [0, rows), n_b <= max_q, n_b <= kv_len[b] <= max_kv, kv_len[b] <= max_pages *
+ * page_size, and every page number used within [0, num_pages).  A sequence
+ * or page that fails is skipped (its rows are not written, a page reads as
+ * zeros) and SAMBA_ERR_BATCH is recorded in the status word.
+ * Limits: page_size 16, 32, 64, 128 or 256; d 16, 32, 64 or 128; num_pages *
+ * Hkv < 2^31; rows and max_kv < 2^30; batch <= 65535; Hkv <= 65535.
+ */
+typedef struct samba_paged_kv {
+  void* k;            /* [num_pages, Hkv, page_size, d] dtype                 */
+  void* v;            /* same                                                 */
+  float* k_scale;     /* [num_pages, Hkv], with SAMBA_E4M3 (else NULL)        */
+  float* v_scale;
+  int64_t num_pages;
+  int32_t page_size, heads_kv, head_dim, dtype;
+} samba_paged_kv;
+
+typedef struct samba_paged_batch {
+  const int32_t* q_start;      /* [batch + 1]                                 */
+  const int32_t* kv_len;       /* [batch]                                     */
+  const int32_t* block_table;  /* [batch, max_pages]                          */
+  int64_t batch, rows;         /* rows: rows of q, k, v, o                    */
+  int64_t max_pages, max_q, max_kv;
+} samba_paged_batch;
+
+/* samba_kv_append: writes the batch's new keys and values into the cache,
+ * with the position rotation of keys and queries applied on the way.  The
+ * rotation turns the first rot_dim elements of each head of q and k by
+ * position p: with angle a_j = p * freqs[j] (j < rot_dim / 2),
+ *   (x_lo, x_hi) -> (x_lo cos a_j - x_hi sin a_j, x_hi cos a_j + x_lo sin a_j)
+ * for the pair (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved.  The
+ * angle is reduced in fp64, the rotation is fp32, and the results are
+ * rounded once (bf16 queries; keys to the cache's type).
+ * With SAMBA_E4M3 the scale of a (page, kv head) is the smallest power of two
+ * s >= 2^-60 with |x| <= 448 s (at most 2^30) for the finite values that this
+ * call stores there, or the scale it had if that is larger and the page already held
+ * earlier positions; if the scale grows, the page's earlier rows are
+ * re-rounded to it.  A page whose row 0 is stored starts afresh.
+ *
+ *   q     [rows, Hq, d] bf16 with row stride ldq, or NULL (no queries)
+ *   k, v  [rows, Hkv, d] bf16 with row strides ldk, ldv
+ *   q_out [rows, Hq, d] bf16 contiguous; may be q if ldq = Hq * d
+ *   freqs [rot_dim / 2] fp64, or NULL with rot_dim 0 (no rotation)
+ * Two sequences of one call must not store into the same page (pages shared
+ * for reading are fine).  Errors: SAMBA_ERR_INVALID_ARG for a null pointer, a bad size, a row
+ * stride below its row or not a multiple of 8, rot_dim not a multiple of 16
+ * within [0, d], or a misaligned pointer; SAMBA_ERR_UNSUPPORTED for the
+ * limits above. */
+typedef struct samba_kv_append_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const double* freqs;
+  int64_t ldq, ldk, ldv;
+  int32_t heads_q, rot_dim, interleaved;
+  samba_paged_kv kv;
+  samba_paged_batch batch;
+} samba_kv_append_args;
+
+int samba_kv_append(const samba_kv_append_args* args, samba_stream_t stream);
+
+/* samba_paged_attn: causal attention of the batch's rows over the cache
+ * (which holds their own keys and values already: samba_kv_append first).
+ * A row at position p attends positions max(0, p - window + 1) .. p, or all
+ * of 0 .. p with window 0, with grouped kv heads as samba_swa_fwd.  Pages
+ * that lie before every window of a sequence's rows are not read, and their
+ * block_table entries may hold anything.  What the cache holds beyond
+ * kv_len is not read as a value (it may be NaN).  Where a call has several
+ * rows of a sequence, a NaN or an infinity in a value that one of them sees
+ * may reach the others (as 0 * NaN); masked keys never matter.
+ *   q, o  [rows, Hq, d] bf16; scale <= 0 selects 1/sqrt(d)
+ * Limits: Hq / Hkv <= 16, max_q * Hq < 2^30, window < 2^30.  The workspace is caller-owned
+ * device memory of samba_paged_attn_workspace_size() bytes, 16-byte aligned,
+ * and needs no initialisation; calls that may run at the same time need
+ * workspaces of their own.  The size depends on the sizes and bounds of the arguments only
+ * (pointers are ignored) and on the number of SMs of the current device.
+ * Errors: SAMBA_ERR_INVALID_ARG for a null pointer, a bad size, Hq not a
+ * multiple of Hkv, a negative window or a misaligned pointer;
+ * SAMBA_ERR_UNSUPPORTED for the limits above; SAMBA_ERR_WORKSPACE for a
+ * missing or short workspace. */
+typedef struct samba_paged_attn_args {
+  const void* q;
+  void* o;
+  int32_t heads_q;
+  float scale;
+  int64_t window;
+  void* workspace;
+  size_t workspace_bytes;
+  samba_paged_kv kv;
+  samba_paged_batch batch;
+} samba_paged_attn_args;
+
+/* SIZE_MAX when the byte count does not fit or the sizes are refused. */
+size_t samba_paged_attn_workspace_size(const samba_paged_attn_args* args);
+
+int samba_paged_attn(const samba_paged_attn_args* args, samba_stream_t stream);
+
+/* ------------------------------------------------------------- block norm
+ * What stands between two blocks of a stack, in one pass over the rows: the
+ * norm after a block, its gate and residual scale, the residual sum and the
+ * norm before the next block.  With rms(x) = x / sqrt(mean(x^2) + eps):
+ *   t  = rms(y) * w_post        (t = y without w_post)
+ *   r' = r + alpha * sigmoid(gate) * t      (factors without a pointer are 1)
+ *   n  = rms(r') * w_pre
+ * per row of `width` elements, in fp32; r' and n are rounded once each (n is
+ * the norm of the unrounded r').  Without y, r' = r (r_out, w_post, gate and
+ * alpha must be NULL): the norm before the first block.  Without n and w_pre
+ * only r' is written.
+ *   r, r_out  [rows, width] r_dtype   (r_out may be r)
+ *   y, gate, n [rows, width] y_dtype
+ *   w_pre, w_post, alpha [width] fp32
+ *   rstd_pre, rstd_post [rows] fp32 or NULL: the factors 1/sqrt(mean + eps)
+ *     of the two norms, for the backward pass
+ * dtypes SAMBA_F32 or SAMBA_BF16; rows 0 .. 2^31 - 1; width a multiple of 8,
+ * 8 .. 8192.
+ * Errors: SAMBA_ERR_INVALID_ARG for a missing or surplus pointer, a bad size
+ * or a misaligned pointer; SAMBA_ERR_UNSUPPORTED for another dtype or a size
+ * above the limits. */
+typedef struct samba_block_norm_args {
+  const void* r;
+  const void* y;
+  const float* w_pre;
+  const float* w_post;
+  const void* gate;
+  const float* alpha;
+  void* r_out;
+  void* n;
+  float* rstd_pre;
+  float* rstd_post;
+  int64_t rows, width;
+  int32_t r_dtype, y_dtype;
+  float eps;
+} samba_block_norm_args;
+
+int samba_block_norm_fwd(const samba_block_norm_args* args, samba_stream_t stream);
+
+/* Gradients of samba_block_norm_fwd.  dn = dL/dn and dr_out = dL/dr' (the
+ * residual stream's own gradient) come in, either may be NULL (zero), and
+ * with x = r' rstd_pre, yh = y rstd_post, s = sigmoid(gate), t as above:
+ *   g = dr_out + rstd_pre (dn w_pre - x mean(dn w_pre x))      dr = g
+ *   dw_pre = sum dn x            dalpha = sum g s t           (sums over rows)
+ *   dgate = alpha g t s (1 - s)  dt = alpha g s               dw_post = sum dt yh
+ *   dy = rstd_post (dt w_post - yh mean(dt w_post yh))        (dt without w_post)
+ * r is the forward's r' (r itself for a call without y); rstd_pre and
+ * rstd_post are the forward's.  Outputs: dr r_dtype (may be dr_out); dy,
+ * dgate y_dtype; dw_pre, dw_post, dalpha [width] fp32.  dy is required with
+ * y, dgate with gate, dw_pre and rstd_pre with dn and w_pre, dw_post and
+ * rstd_post with w_post, dalpha with alpha.  dr, dy and dgate are rounded
+ * once; every sum is fp32 and in a fixed order, so results repeat bit for bit
+ * on one device.  The workspace (samba_block_norm_bwd_workspace_size()
+ * bytes, 16-byte aligned, no initialisation) holds the blocks' column sums.
+ * Errors as samba_block_norm_fwd, and SAMBA_ERR_WORKSPACE. */
+typedef struct samba_block_norm_bwd_args {
+  const void* dn;
+  const void* dr_out;
+  const void* r;
+  const float* w_pre;
+  const float* rstd_pre;
+  const void* y;
+  const float* w_post;
+  const float* rstd_post;
+  const void* gate;
+  const float* alpha;
+  void* dr;
+  void* dy;
+  void* dgate;
+  float* dw_pre;
+  float* dw_post;
+  float* dalpha;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t rows, width;
+  int32_t r_dtype, y_dtype;
+} samba_block_norm_bwd_args;
+
+/* 0 for a non-positive size. */
+size_t samba_block_norm_bwd_workspace_size(int64_t rows, int64_t width);
+
+int samba_block_norm_bwd(const samba_block_norm_bwd_args* args, samba_stream_t stream);
 
 #ifdef __cplusplus
 }
