@@ -423,20 +423,23 @@ def swa_step(q_t, k_t, v_t, k_ring, v_ring, pos, window, scale=None, o_t=None, w
 
 
 # ------------------------------------------------------------- paged cache
-def _placed(named, stream):
-    """Checks that the tensors are on one device and the stream (if given) too;
-    returns a guard that makes the device current."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _same(t, name, dtype, shape, dev):
+    """_need, and that the tensor is on device number ``dev``; one test where all
+    is well (these calls take microseconds)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+
+
+def _here(dev, stream):
+    """A guard that makes device number ``dev`` current; refuses another device's stream."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return _NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_NO_GUARD = contextlib.nullcontext()
 
 
 def _lend(stream, *tensors):
@@ -469,7 +472,10 @@ class PagedKv:
             raise ValueError("k_scale and v_scale go with an 8-bit cache, and only with it")
         _opt(k_scale, "k_scale", torch.float32, (n, h))
         _opt(v_scale, "v_scale", torch.float32, (n, h))
-        _placed((("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)), None)
+        self.device = k.get_device()
+        for t, name in ((v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _same(t, name, t.dtype, t.shape, self.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.args = L.PagedKvArgs(L.ptr(k), L.ptr(v), L.ptr(k_scale), L.ptr(v_scale), n, p, h, d, codes[k.dtype])
 
@@ -498,7 +504,9 @@ class PagedBatch:
         _need(block_table, "block_table", torch.int32)
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"block_table must be [{B}, max_pages]")
-        _placed((("q_start", q_start), ("kv_len", kv_len), ("block_table", block_table)), None)
+        self.device = kv_len.get_device()
+        _same(q_start, "q_start", torch.int32, q_start.shape, self.device)
+        _same(block_table, "block_table", torch.int32, block_table.shape, self.device)
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
         self.max_q, self.max_kv = int(max_q), int(max_kv)
         if self.max_q < 0 or self.max_kv < 0:
@@ -506,25 +514,29 @@ class PagedBatch:
         self.args = L.PagedBatchArgs(L.ptr(q_start), L.ptr(kv_len), L.ptr(block_table), B, 0, block_table.shape[1],
                                      self.max_q, self.max_kv)
 
-    def _with_rows(self, rows):
-        a = self.args
-        return L.PagedBatchArgs(a.q_start, a.kv_len, a.block_table, a.batch, rows, a.max_pages, a.max_q, a.max_kv)
 
-
-def _head_rows(t, name, heads, dim):
+def _head_rows(t, name, heads, dim, dev):
     """Checks a [T, heads, dim] bf16 matrix of heads with any row stride; returns that stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have shape [rows, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
-    h = t.shape[1]
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != dim):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda
+                         else f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or shape[1] != (heads or shape[1]):
+        raise ValueError(f"{name} must have shape [rows, {heads or 'heads'}, {dim}], got {tuple(shape)}")
+    ld, hs, es = t.stride()
+    if es != 1 or (hs != dim and shape[1] > 1):
         raise ValueError(f"{name} needs contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else h * dim
+    return ld if shape[0] > 1 else shape[1] * dim
+
+
+def _same_device(cache, batch):
+    if cache.device != batch.device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the batch on cuda:{batch.device}")
+    return cache.device
 
 
 def kv_append(q, k, v, cache, batch, freqs=None, interleaved=False, q_out=None, stream=None):
@@ -534,55 +546,49 @@ def kv_append(q, k, v, cache, batch, freqs=None, interleaved=False, q_out=None, 
     ranges of one matrix (rows strided).  ``freqs`` [rot / 2] fp64: the angle
     of a pair is position * freqs[j]; None: no rotation.  Returns the rotated
     queries [T, Hq, d] (rows of no sequence are not written)."""
-    kv = cache.args
-    ldk = _head_rows(k, "k", kv.heads_kv, kv.head_dim)
-    ldv = _head_rows(v, "v", kv.heads_kv, kv.head_dim)
+    kv, dev = cache.args, _same_device(cache, batch)
+    dim = kv.head_dim
+    ldk = _head_rows(k, "k", kv.heads_kv, dim, dev)
+    ldv = _head_rows(v, "v", kv.heads_kv, dim, dev)
     rows = k.shape[0]
     if v.shape[0] != rows:
         raise ValueError("k and v disagree on their rows")
-    ldq = heads_q = 0
+    ldq = heads_q = rot = 0
     if q is not None:
-        ldq = _head_rows(q, "q", None, kv.head_dim)
+        ldq = _head_rows(q, "q", None, dim, dev)
         heads_q = q.shape[1]
         if q.shape[0] != rows or heads_q < 1:
             raise ValueError("q needs the rows of k and v, and a head")
         if q_out is not None:
-            _need(q_out, "q_out", torch.bfloat16, q.shape)
+            _same(q_out, "q_out", torch.bfloat16, q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    rot = 0
     if freqs is not None:
-        _need(freqs, "freqs", torch.float64)
+        _same(freqs, "freqs", torch.float64, freqs.shape, dev)
         rot = 2 * freqs.numel()
         if freqs.dim() != 1 or rot < 1:
             raise ValueError("freqs must be [rot / 2]")
-    named = (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("freqs", freqs), ("the cache", cache.k),
-             ("the batch", batch.kv_len))
-    with _placed(named, stream):
+    with _here(dev, stream):
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
             _lend(stream, q_out)
         if rows == 0 or batch.args.batch == 0:
             return q_out
-        a = L.KvAppendArgs(L.ptr(q), L.ptr(k), L.ptr(v), L.ptr(q_out), L.ptr(freqs), ldq, ldk, ldv, heads_q, rot,
-                           1 if interleaved else 0, kv, batch._with_rows(rows))
+        a = L.KvAppendArgs(L.ptr(q), k.data_ptr(), v.data_ptr(), L.ptr(q_out), L.ptr(freqs), ldq, ldk, ldv, heads_q,
+                           rot, 1 if interleaved else 0, kv, batch.args)
+        a.batch.rows = rows
         L.check(L.load().samba_kv_append(ctypes.byref(a), L.stream_handle(stream)))
     return q_out
 
 
-def _paged_attn_struct(batch, cache, heads_q, window, rows=0, scale=None):
-    a = L.PagedAttnArgs()
-    a.heads_q, a.window, a.scale = int(heads_q), int(window), float(scale) if scale else 0.0
-    a.kv, a.batch = cache.args, batch._with_rows(rows)
-    return a
-
-
 def paged_attn_workspace_size(batch, cache, heads_q, window=0) -> int:
     """Bytes of workspace of paged_attn for these bounds (0: none)."""
-    with _placed((("the cache", cache.k), ("the batch", batch.kv_len)), None):
-        n = L.load().samba_paged_attn_workspace_size(ctypes.byref(_paged_attn_struct(batch, cache, heads_q, window)))
+    with _here(_same_device(cache, batch), None):
+        lib = L.load()
+        n = lib.samba_paged_attn_workspace_size(
+            ctypes.byref(L.PagedAttnArgs(None, None, int(heads_q), 0.0, int(window), None, 0, cache.args, batch.args)))
         if n == ctypes.c_size_t(-1).value:
-            raise L.SambaError(L.SAMBA_ERR_UNSUPPORTED, L.load().samba_last_error().decode() or "workspace too large")
+            raise L.SambaError(L.SAMBA_ERR_UNSUPPORTED, lib.samba_last_error().decode() or "workspace too large")
     return int(n)
 
 
@@ -591,38 +597,51 @@ def paged_attn(q, cache, batch, window=0, scale=None, o=None, workspace=None, st
     cache (which holds their keys and values already): the last ``window``
     positions, or all with 0 (see samba_paged_attn).  Returns o (rows of no
     sequence are not written)."""
-    kv = cache.args
-    _need(q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != kv.head_dim or q.shape[1] < 1:
-        raise ValueError(f"q must have shape [rows, heads, {kv.head_dim}], got {tuple(q.shape)}")
-    _opt(o, "o", torch.bfloat16, q.shape)
-    _opt(workspace, "workspace", torch.uint8)
-    with _placed((("q", q), ("the cache", cache.k), ("the batch", batch.kv_len), ("o", o), ("workspace", workspace)),
-                 stream):
+    kv, dev = cache.args, _same_device(cache, batch)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != kv.head_dim or q.shape[1] < 1:
+        raise ValueError(f"q must be a [rows, heads, {kv.head_dim}] tensor")
+    rows, heads, _ = shape = q.shape
+    _same(q, "q", torch.bfloat16, shape, dev)
+    if o is not None:
+        _same(o, "o", torch.bfloat16, shape, dev)
+    if workspace is not None:
+        _same(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    with _here(dev, stream):
         lib = L.load()
-        a = _paged_attn_struct(batch, cache, q.shape[1], window, q.shape[0], scale)
         if o is None:
             o = torch.empty_like(q)
             _lend(stream, o)
-        if q.shape[0] == 0 or batch.args.batch == 0:
+        if rows == 0 or batch.args.batch == 0:
             return o
         if workspace is None:
-            n = lib.samba_paged_attn_workspace_size(ctypes.byref(a))
-            if 0 < n < ctypes.c_size_t(-1).value:
+            n = paged_attn_workspace_size(batch, cache, heads, window)
+            if n > 0:
                 workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
                 _lend(stream, workspace)
-        a.q, a.o, a.workspace = L.ptr(q), L.ptr(o), L.ptr(workspace)
-        a.workspace_bytes = 0 if workspace is None else workspace.numel()
+        a = L.PagedAttnArgs(q.data_ptr(), o.data_ptr(), heads, float(scale) if scale else 0.0, int(window),
+                            L.ptr(workspace), 0 if workspace is None else workspace.numel(), kv, batch.args)
+        a.batch.rows = rows
         L.check(lib.samba_paged_attn(ctypes.byref(a), L.stream_handle(stream)))
     return o
 
 
 # -------------------------------------------------------------- block norm
 def _norm_rows(r):
+    """Checks the residual stream; returns its shape, rows, width, type's code and device."""
     if not isinstance(r, torch.Tensor) or r.dim() < 1:
         raise ValueError("r must be a [..., width] tensor")
-    C = r.shape[-1]
-    return r.numel() // C if C else 0, C
+    _need(r, "r")
+    shape = r.shape
+    C = shape[-1]
+    return shape, r.numel() // C if C else 0, C, L.dtype_code(r), r.get_device()
+
+
+def _norm_code(dt):
+    if dt is torch.bfloat16:
+        return L.SAMBA_BF16
+    if dt is not torch.float32:
+        raise TypeError(f"unsupported dtype {dt}")
+    return L.SAMBA_F32
 
 
 def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, eps=1e-6, r_out=None, n=None,
@@ -634,45 +653,40 @@ def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, ep
     default).  ``rstd_pre`` / ``rstd_post`` ([rows] fp32) receive the row
     factors for block_norm_bwd.  Returns (r', n); n is None without w_pre, r'
     is r without y."""
-    M, C = _norm_rows(r)
-    _need(r, "r")
-    L.dtype_code(r)
-    _opt(y, "y", None, r.shape)
-    ydt = y.dtype if y is not None else (n.dtype if n is not None else n_dtype or r.dtype)
-    if y is not None and n_dtype is not None and n_dtype != y.dtype:
-        raise TypeError("n has y's dtype")
-    _opt(gate, "gate", ydt, r.shape)
-    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (alpha, "alpha")):
-        _opt(t, name, torch.float32, (C,))
+    shape, M, C, rcode, dev = _norm_rows(r)
+    f32 = torch.float32
+    if y is not None:
+        ydt = y.dtype
+        _same(y, "y", ydt, shape, dev)
+        if n_dtype is not None and n_dtype != ydt:
+            raise TypeError("n has y's dtype")
+    else:
+        ydt = n.dtype if n is not None else n_dtype or r.dtype
+    ycode = _norm_code(ydt)
     if w_pre is None and (n is not None or rstd_pre is not None):
         raise ValueError("n and rstd_pre go with w_pre")
-    _opt(r_out, "r_out", r.dtype, r.shape)
-    _opt(n, "n", ydt, r.shape)
-    _opt(rstd_pre, "rstd_pre", torch.float32, (M,))
-    _opt(rstd_post, "rstd_post", torch.float32, (M,))
-    with _placed((("r", r), ("y", y), ("w_pre", w_pre), ("w_post", w_post), ("gate", gate), ("alpha", alpha),
-                  ("r_out", r_out), ("n", n), ("rstd_pre", rstd_pre), ("rstd_post", rstd_post)), stream):
+    for t, name, dt, sh in ((w_pre, "w_pre", f32, (C,)), (w_post, "w_post", f32, (C,)), (alpha, "alpha", f32, (C,)),
+                            (gate, "gate", ydt, shape), (r_out, "r_out", r.dtype, shape), (n, "n", ydt, shape),
+                            (rstd_pre, "rstd_pre", f32, (M,)), (rstd_post, "rstd_post", f32, (M,))):
+        if t is not None:
+            _same(t, name, dt, sh, dev)
+    with _here(dev, stream):
         if y is not None and r_out is None:
             r_out = torch.empty_like(r)
             _lend(stream, r_out)
         if w_pre is not None and n is None:
-            n = torch.empty(r.shape, dtype=ydt, device=r.device)
+            n = torch.empty_like(r, dtype=ydt)
             _lend(stream, n)
-        a = L.BlockNormArgs(L.ptr(r), L.ptr(y), L.ptr(w_pre), L.ptr(w_post), L.ptr(gate), L.ptr(alpha), L.ptr(r_out),
-                            L.ptr(n), L.ptr(rstd_pre), L.ptr(rstd_post), M, C, L.dtype_code(r), _norm_code(ydt),
-                            float(eps))
         if M > 0:
+            p = L.ptr
+            a = L.BlockNormArgs(r.data_ptr(), p(y), p(w_pre), p(w_post), p(gate), p(alpha), p(r_out), p(n), p(rstd_pre),
+                                p(rstd_post), M, C, rcode, ycode, eps)
             L.check(L.load().samba_block_norm_fwd(ctypes.byref(a), L.stream_handle(stream)))
     return (r if y is None else r_out), n
 
 
-def _norm_code(dt):
-    if dt not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {dt}")
-    return L.SAMBA_F32 if dt == torch.float32 else L.SAMBA_BF16
-
-
 def block_norm_bwd_workspace_size(rows, width) -> int:
+    """Bytes of workspace of block_norm_bwd on the current device."""
     return int(L.load().samba_block_norm_bwd_workspace_size(rows, width))
 
 
@@ -682,9 +696,8 @@ def block_norm_bwd(dn, r, w_pre=None, rstd_pre=None, dr_out=None, y=None, w_post
     and dr_out = dL/dr' (either may be None): r is the forward's r', rstd_pre
     and rstd_post its row factors.  Returns a dict with dr, dw_pre and, where
     the forward input exists, dy, dw_post, dgate, dalpha."""
-    M, C = _norm_rows(r)
-    _need(r, "r")
-    rcode = L.dtype_code(r)
+    shape, M, C, rcode, dev = _norm_rows(r)
+    f32, rdt = torch.float32, r.dtype
     if dn is None and dr_out is None:
         raise ValueError("one of dn and dr_out is needed")
     if dn is not None and (w_pre is None or rstd_pre is None):
@@ -693,40 +706,40 @@ def block_norm_bwd(dn, r, w_pre=None, rstd_pre=None, dr_out=None, y=None, w_post
         raise ValueError("w_post, gate and alpha go with y")
     if w_post is not None and rstd_post is None:
         raise ValueError("w_post needs rstd_post")
-    ydt = y.dtype if y is not None else dn.dtype if dn is not None else r.dtype
-    _opt(dn, "dn", ydt, r.shape)
-    _opt(dr_out, "dr_out", r.dtype, r.shape)
-    _opt(y, "y", ydt, r.shape)
-    _opt(gate, "gate", ydt, r.shape)
-    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (alpha, "alpha")):
-        _opt(t, name, torch.float32, (C,))
-    _opt(rstd_pre, "rstd_pre", torch.float32, (M,))
-    _opt(rstd_post, "rstd_post", torch.float32, (M,))
-    _opt(workspace, "workspace", torch.uint8)
-    with _placed((("r", r), ("dn", dn), ("dr_out", dr_out), ("y", y), ("gate", gate), ("w_pre", w_pre),
-                  ("w_post", w_post), ("alpha", alpha), ("rstd_pre", rstd_pre), ("rstd_post", rstd_post),
-                  ("workspace", workspace)), stream):
-        def vec(on):
-            return torch.empty((C,), dtype=torch.float32, device=r.device) if on else None
-
-        out = {"dr": torch.empty_like(r), "dy": None if y is None else torch.empty_like(y),
-               "dgate": None if gate is None else torch.empty_like(gate), "dw_pre": vec(dn is not None),
-               "dw_post": vec(w_post is not None), "dalpha": vec(alpha is not None)}
+    ydt = y.dtype if y is not None else dn.dtype if dn is not None else rdt
+    ycode = _norm_code(ydt)
+    for t, name, dt, sh in ((dn, "dn", ydt, shape), (dr_out, "dr_out", rdt, shape), (y, "y", ydt, shape),
+                            (gate, "gate", ydt, shape), (w_pre, "w_pre", f32, (C,)), (w_post, "w_post", f32, (C,)),
+                            (alpha, "alpha", f32, (C,)), (rstd_pre, "rstd_pre", f32, (M,)),
+                            (rstd_post, "rstd_post", f32, (M,))):
+        if t is not None:
+            _same(t, name, dt, sh, dev)
+    if workspace is not None:
+        _same(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    with _here(dev, stream):
+        like, empty = torch.empty_like, torch.empty
+        dr = like(r)
+        dy = None if y is None else like(y)
+        dgate = None if gate is None else like(gate)
+        dw_pre = None if dn is None else empty((C,), dtype=f32, device=r.device)
+        dw_post = None if w_post is None else like(w_post)
+        dalpha = None if alpha is None else like(alpha)
+        out = {"dr": dr, "dy": dy, "dgate": dgate, "dw_pre": dw_pre, "dw_post": dw_post, "dalpha": dalpha}
         if M == 0:
-            for key in ("dw_pre", "dw_post", "dalpha"):
-                if out[key] is not None:
-                    out[key].zero_()
+            for t in (dw_pre, dw_post, dalpha):
+                if t is not None:
+                    t.zero_()
             return out
         if workspace is None:
-            workspace = torch.empty((max(block_norm_bwd_workspace_size(M, C), 16),), dtype=torch.uint8, device=r.device)
+            workspace = empty((max(block_norm_bwd_workspace_size(M, C), 16),), dtype=torch.uint8, device=r.device)
             _lend(stream, workspace)
         _lend(stream, *out.values())
-        a = L.BlockNormBwdArgs(L.ptr(dn), L.ptr(dr_out), L.ptr(r), L.ptr(w_pre) if dn is not None else None,
-                               L.ptr(rstd_pre) if dn is not None else None, L.ptr(y), L.ptr(w_post),
-                               L.ptr(rstd_post) if w_post is not None else None, L.ptr(gate), L.ptr(alpha),
-                               L.ptr(out["dr"]), L.ptr(out["dy"]), L.ptr(out["dgate"]), L.ptr(out["dw_pre"]),
-                               L.ptr(out["dw_post"]), L.ptr(out["dalpha"]), L.ptr(workspace), workspace.numel(), M, C,
-                               rcode, _norm_code(ydt))
+        p = L.ptr
+        a = L.BlockNormBwdArgs(p(dn), p(dr_out), r.data_ptr(), None if dn is None else w_pre.data_ptr(),
+                               None if dn is None else rstd_pre.data_ptr(), p(y), p(w_post),
+                               None if w_post is None else rstd_post.data_ptr(), p(gate), p(alpha), dr.data_ptr(), p(dy),
+                               p(dgate), p(dw_pre), p(dw_post), p(dalpha), workspace.data_ptr(), workspace.numel(), M, C,
+                               rcode, ycode)
         L.check(L.load().samba_block_norm_bwd(ctypes.byref(a), L.stream_handle(stream)))
     return out
 
