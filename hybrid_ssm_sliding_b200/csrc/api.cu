@@ -91,8 +91,9 @@ const char* samba_last_error(void) { return g_last_error.c_str(); }
 
 int samba_get_status(samba_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int codes[8] = {take_status_scan(s),    take_status_swa(s),       take_status_misc(s),       take_status_gemm(s),
-                  take_status_swa_bwd(s), take_status_kv_append(s), take_status_paged_attn(s), take_status_block_norm(s)};
+  int codes[9] = {take_status_scan(s),       take_status_swa(s),         take_status_misc(s),
+                  take_status_gemm(s),       take_status_swa_bwd(s),     take_status_kv_append(s),
+                  take_status_paged_attn(s), take_status_paged_chunk(s), take_status_block_norm(s)};
   for (int c : codes)
     if (c == SAMBA_ERR_CUDA) return fail(SAMBA_ERR_CUDA, "samba_get_status: %s", cudaGetErrorString(cudaGetLastError()));
   for (int c : codes)

@@ -95,6 +95,7 @@ int take_status_kv_append(cudaStream_t s);
 size_t paged_attn_workspace(const samba_paged_attn_args& a);
 int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t stream);
 int take_status_paged_attn(cudaStream_t s);
+int take_status_paged_chunk(cudaStream_t s);
 size_t block_norm_bwd_workspace(int64_t rows, int64_t C);
 int launch_block_norm_fwd(const samba_block_norm_args& a, cudaStream_t stream);
 int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t stream);

@@ -29,6 +29,7 @@
 
 #include "paged.cuh"
 #include "host.hpp"
+#include "paged_plan.hpp"
 #include "pdl.cuh"
 
 namespace samba {
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
     uint64_t* bar = &mybar[it % STG];
     mbar_arrive_expect_tx(bar, Cfg::STAGE);
     for (int r = 0; r < SW; r += brows) {
-      const int pi = (j + r) / P - pg0;
+      const int pi = ((j + r) >> p.page_shift) - pg0;
       const int pg = pi < npg ? tab[pi] : static_cast<int>(p.num_pages);  // num_pages: past the pool, read as zeros
       const int blk = pg * p.Hkv + g, row = (j + r) & (P - 1);
 #pragma unroll
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
         }
-        const int pi = (j0 + 16 * u) / P - pg0;
+        const int pi = ((j0 + 16 * u) >> p.page_shift) - pg0;
         const float2 sc = pi < npg ? sct[pi] : make_float2(1.f, 0.f);
         kv_e[u] = sc.y;
         inv_v[u] = exp2i(-static_cast<int>(sc.y));
@@ -623,9 +624,9 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
 }
 
 // ------------------------------------------------------------------ launcher
-struct PagedPlan {
-  int nt, ntile, nsplit, chunk;
-};
+// Query rows a kv head up to which a call goes through the split kernel here:
+// its tiles of 16 rows each read the keys again.
+constexpr int64_t kFewRows = 64;
 
 // Positions a split: the range of one row tile over as many splits as fill
 // the SMs four blocks deep, at least 128 (a warp's 32) and at most 2048 (which bounds
@@ -634,6 +635,17 @@ static PagedPlan paged_plan(const samba_paged_attn_args& a) {
   PagedPlan pl;
   const int64_t group = a.heads_q / a.kv.heads_kv;
   const int64_t rows = std::max<int64_t>(1, a.batch.max_q) * group;
+  pl.chunk_kernel = rows > kFewRows;
+  if (pl.chunk_kernel) {
+    // one block an SM: key tiles are split while units leave SMs idle, at least four tiles each
+    pl.nt = pl.chunk = 0;
+    pl.ntile = (int)((rows + 255) / 256);
+    int64_t span = a.batch.max_kv;
+    if (a.window > 0) span = std::min<int64_t>(span, a.window + 256 / group + 128);
+    const int64_t units = (int64_t)pl.ntile * a.kv.heads_kv * std::max<int64_t>(1, a.batch.batch);
+    pl.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm_count() / units, span / 512));
+    return pl;
+  }
   pl.nt = rows <= 8 ? 1 : 2;
   pl.ntile = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
   int64_t span = std::max<int64_t>(1, a.batch.max_kv);
@@ -692,11 +704,7 @@ static int paged_go(const samba_paged_attn_args& a, const PagedPlan& pl, PagedPa
   if (rc) return rc;
   const int64_t gx = a.batch.batch * pl.ntile * pl.nsplit;
   if (gx > INT32_MAX) return fail(SAMBA_ERR_UNSUPPORTED, "samba_paged_attn: too many rows");
-  cudaError_t e = launch_pdl(kern, dim3((unsigned)gx, a.kv.heads_kv), dim3(128), smem, s, mk, mv, p);
-  if (e == cudaSuccess && pl.nsplit > 1) {
-    const int64_t cx = (a.batch.max_q * a.heads_q + 3) / 4;
-    e = launch_pdl(paged_combine_kernel<HD>, dim3((unsigned)cx, (unsigned)a.batch.batch), dim3(128), 0, s, p, P);
-  }
+  const cudaError_t e = launch_pdl(kern, dim3((unsigned)gx, a.kv.heads_kv), dim3(128), smem, s, mk, mv, p);
   if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "samba_paged_attn: launch failed: %s", cudaGetErrorString(e));
   return check_launch("samba_paged_attn");
 }
@@ -704,13 +712,25 @@ static int paged_go(const samba_paged_attn_args& a, const PagedPlan& pl, PagedPa
 template <int HD>
 static int paged_hd(const samba_paged_attn_args& a, const PagedPlan& pl, PagedParams& p, cudaStream_t s) {
   const bool kv8 = a.kv.dtype == SAMBA_E4M3;
-  if (pl.nt == 1) return kv8 ? paged_go<HD, true, 1>(a, pl, p, s) : paged_go<HD, false, 1>(a, pl, p, s);
-  return kv8 ? paged_go<HD, true, 2>(a, pl, p, s) : paged_go<HD, false, 2>(a, pl, p, s);
+  int rc = SAMBA_OK;
+  if (pl.chunk_kernel) {}  // its splits are there already
+  else if (pl.nt == 1) rc = kv8 ? paged_go<HD, true, 1>(a, pl, p, s) : paged_go<HD, false, 1>(a, pl, p, s);
+  else rc = kv8 ? paged_go<HD, true, 2>(a, pl, p, s) : paged_go<HD, false, 2>(a, pl, p, s);
+  if (rc != SAMBA_OK || pl.nsplit == 1) return rc;
+  const int64_t cx = (a.batch.max_q * a.heads_q + 3) / 4;
+  const cudaError_t e = launch_pdl(paged_combine_kernel<HD>, dim3((unsigned)cx, (unsigned)a.batch.batch), dim3(128), 0, s, p,
+                                   (int)a.kv.page_size);
+  if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "samba_paged_attn: launch failed: %s", cudaGetErrorString(e));
+  return check_launch("samba_paged_attn");
 }
 
 int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t s) {
   if (a.batch.batch == 0 || a.batch.rows == 0 || a.batch.max_q == 0) return SAMBA_OK;
   const PagedPlan pl = paged_plan(a);
+  if (pl.chunk_kernel) {
+    const int rc = launch_paged_chunk(a, pl, s);
+    if (rc != SAMBA_OK || pl.nsplit == 1) return rc;
+  }
   PagedParams p;
   p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
   p.o = reinterpret_cast<__nv_bfloat16*>(a.o);
@@ -727,8 +747,7 @@ int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t s) {
   p.ntile = pl.ntile;
   p.nsplit = pl.nsplit;
   p.chunk = pl.chunk;
-  const float scale = a.scale > 0.f ? a.scale : 1.f / std::sqrt((float)a.kv.head_dim);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = paged_scale_log2(a);
   switch (a.kv.head_dim) {
     case 16: return paged_hd<16>(a, pl, p, s);
     case 32: return paged_hd<32>(a, pl, p, s);

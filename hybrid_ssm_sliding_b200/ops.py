@@ -440,6 +440,7 @@ def _here(dev, stream):
 
 
 _NO_GUARD = contextlib.nullcontext()
+_SIZE_MAX = ctypes.c_size_t(-1).value
 
 
 def _lend(stream, *tensors):
@@ -587,7 +588,7 @@ def paged_attn_workspace_size(batch, cache, heads_q, window=0) -> int:
         lib = L.load()
         n = lib.samba_paged_attn_workspace_size(
             ctypes.byref(L.PagedAttnArgs(None, None, int(heads_q), 0.0, int(window), None, 0, cache.args, batch.args)))
-        if n == ctypes.c_size_t(-1).value:
+        if n == _SIZE_MAX:
             raise L.SambaError(L.SAMBA_ERR_UNSUPPORTED, lib.samba_last_error().decode() or "workspace too large")
     return int(n)
 
@@ -613,14 +614,15 @@ def paged_attn(q, cache, batch, window=0, scale=None, o=None, workspace=None, st
             _lend(stream, o)
         if rows == 0 or batch.args.batch == 0:
             return o
-        if workspace is None:
-            n = paged_attn_workspace_size(batch, cache, heads, window)
-            if n > 0:
-                workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
-                _lend(stream, workspace)
         a = L.PagedAttnArgs(q.data_ptr(), o.data_ptr(), heads, float(scale) if scale else 0.0, int(window),
                             L.ptr(workspace), 0 if workspace is None else workspace.numel(), kv, batch.args)
         a.batch.rows = rows
+        if workspace is None:
+            n = lib.samba_paged_attn_workspace_size(ctypes.byref(a))
+            if 0 < n < _SIZE_MAX:  # otherwise none is needed, or the call says what is wrong
+                workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+                _lend(stream, workspace)
+                a.workspace, a.workspace_bytes = workspace.data_ptr(), n
         L.check(lib.samba_paged_attn(ctypes.byref(a), L.stream_handle(stream)))
     return o
 
