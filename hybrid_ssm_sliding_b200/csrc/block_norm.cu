@@ -15,9 +15,10 @@
 // The backward pass needs one joint sum a row: with c = alpha s w_post yh and
 // s1 = sum dn w_pre x, the second norm's sum is
 //   sum c g = sum c (dr' + rstd dn w_pre) - rstd s1 / C sum c x.
-// The column sums (dw_pre, dw_post, dalpha) stay in registers over all rows of
-// a block; each block writes them once and a second kernel adds the blocks in
-// a fixed order (no atomics, so results repeat bit for bit).
+// dw_post = alpha S and dalpha = w_post S share the column sums S = sum g s yh.
+// They and dw_pre's stay in registers over all rows of a block; each block
+// writes them once and a second kernel adds the blocks in a fixed order (no
+// atomics, so results repeat bit for bit).
 #include <algorithm>
 
 #include "common.cuh"
@@ -60,30 +61,34 @@ constexpr int kNormMaxStages = 4;
 struct NormShared {
   uint64_t full[kNormMaxStages];
   int abort_flag, pad[3];
-  float slots[2][32][4];
+  float slots[2][3][32];
 };
 constexpr int kNormHead = (int)((sizeof(NormShared) + 127) / 128 * 128);
 
 // Sums of N values over the warps of a row, the same bits in every thread.
 // `ph` alternates between two slots, so one barrier per call is enough: a slot
 // is written again only after the barrier of the call in between.
+struct RowWarps {
+  int nw, w0, width;  // warps a row, the first of this row, the power of two from nw
+  __device__ RowWarps(int tpr) : nw(tpr >> 5), w0((threadIdx.x >> 5) / nw * nw), width(1) {
+    while (width < nw) width *= 2;
+  }
+};
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], NormShared& sh, int& ph, int tpr) {
+__device__ __forceinline__ void row_sum(float (&v)[N], NormShared& sh, int& ph, const RowWarps& rw) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int nw = tpr >> 5;
-  if (nw == 1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / nw * nw;
+  if (rw.nw == 1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (rw.width - 1);
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) sh.slots[ph][warp][i] = v[i];
+    for (int i = 0; i < N; ++i) sh.slots[ph][i][warp] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < nw ? sh.slots[ph][w0 + lane][i] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < N; ++i) v[i] = k < rw.nw ? sh.slots[ph][i][rw.w0 + k] : 0.f;
+  for (int o = rw.width >> 1; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   ph ^= 1;
@@ -117,46 +122,48 @@ __device__ __forceinline__ void norm_issue(const NormInputs<NTEN>& in, const Nor
                 &sh.full[stage]);
 }
 
-// Walks over this block's groups: body(row, in, at) where `at(i)` is tensor
-// i's first element of the thread's row (in the ring or in global memory) and
-// read() has to run it before the stage is released.  READ loads a row's
-// values into registers; BODY computes with them.
+// Walks over this block's groups of rows: read(at) loads the thread's row into
+// registers, at(i) being tensor i's row (in the ring, whose stage is refilled
+// once all have read, or in global memory); body(row, live) computes with them.
+// Threads without a row (behind the last one) keep an earlier row's values and
+// store nothing.
 template <bool RING, int NTEN, class Read, class Body>
 __device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
                                           unsigned char* ring, Read&& read, Body&& body) {
   const int sub = threadIdx.x / s.tpr;
-  int64_t first = blockIdx.x;
-  if constexpr (RING) {
-    if (threadIdx.x == 0)
-      for (int i = 0; i < s.stages && first + (int64_t)i * gridDim.x < s.groups; ++i)
-        norm_issue(in, s, sh, ring, first + (int64_t)i * gridDim.x, i);
-  }
-  int stage = 0, parity = 0;
-  for (int64_t g = first; g < s.groups; g += gridDim.x) {
+  int64_t g = blockIdx.x;
+  if constexpr (!RING) {  // as many blocks as groups
     const int64_t row = g * s.rpb + sub;
-    const bool live = row < s.rows;
-    if constexpr (RING) {
-      const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort_flag);
-      if (ok && live)
-        read(row, [&](int i) { return ring + stage * s.stage_bytes + s.off[i] + (int64_t)sub * s.C * in.t[i].elem; });
-      if (!__syncthreads_and(ok)) {  // a wait gave up: leave once the copies in flight have landed
-        if (threadIdx.x == 0) {
-          volatile int never = 0;
-          int64_t h = g + gridDim.x;
-          for (int i = 1; i < s.stages && h < s.groups; ++i, h += gridDim.x) {
-            const int st = (stage + i) % s.stages;
-            mbar_wait(&sh.full[st], parity ^ (stage + i >= s.stages ? 1 : 0), &never);
-          }
-        }
-        return;
+    if (row < s.rows)
+      read([&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + row * s.C * in.t[i].elem; });
+    body(row, row < s.rows);
+    return;
+  }
+  if (threadIdx.x == 0)
+    for (int i = 0; i < s.stages && g + (int64_t)i * gridDim.x < s.groups; ++i)
+      norm_issue(in, s, sh, ring, g + (int64_t)i * gridDim.x, i);
+  int off[NTEN];
+#pragma unroll
+  for (int i = 0; i < NTEN; ++i) off[i] = s.off[i] + sub * s.C * in.t[i].elem;
+  int stage = 0, parity = 0;
+  for (; g < s.groups; g += gridDim.x) {
+    const int64_t row = g * s.rpb + sub;
+    const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort_flag);
+    const unsigned char* base = ring + stage * s.stage_bytes;
+    if (row < s.rows) read([&](int i) { return base + off[i]; });
+    if (!__syncthreads_and(ok)) {  // a wait gave up: leave once the copies in flight have landed
+      if (threadIdx.x == 0) {
+        volatile int never = 0;
+        int64_t h = g + gridDim.x;
+        for (int i = 1; i < s.stages && h < s.groups; ++i, h += gridDim.x)
+          mbar_wait(&sh.full[(stage + i) % s.stages], parity ^ (stage + i >= s.stages ? 1 : 0), &never);
       }
-      if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
-        norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
-      if (++stage == s.stages) stage = 0, parity ^= 1;
-    } else if (live) {
-      read(row, [&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + row * s.C * in.t[i].elem; });
+      return;
     }
-    body(row, live);
+    if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
+      norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
+    if (++stage == s.stages) stage = 0, parity ^= 1;
+    body(row, row < s.rows);
   }
 }
 
@@ -205,12 +212,21 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
   const int e[2] = {4 * lt, 4 * (lt + s.tpr)};
   const bool has[2] = {e[0] < s.C, e[1] < s.C};
   const bool has_y = p.in.t[1].p != nullptr, has_g = p.in.t[2].p != nullptr;
+  const RowWarps rw(s.tpr);
   norm_setup<RING>(sh, s);
-  float r[8], y[8], z[8];
+  float wa[8], wp[8];  // w_post alpha, w_pre
+  load_vec(wa, p.w_post, e, has);
+  load_vec(wp, p.alpha, e, has);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wa[i] *= wp[i];
+  load_vec(wp, p.w_pre, e, has);
+  float r[8], y[8], z[8];  // elements that the row does not have stay zero
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = y[i] = z[i] = 0.f;
   int ph = 0;
   norm_walk<RING>(
       p.in, s, sh, sm + kNormHead,
-      [&](int64_t, auto at) {
+      [&](auto at) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
@@ -221,47 +237,45 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
       },
       [&](int64_t row, bool live) {
         float sum[1];
+        const int64_t o = row * s.C;
         if (has_y) {
+          sum[0] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sum[0] = fmaf(y[i], y[i], sum[0]);
+            y[i] *= wa[i];
+          }
+          if (has_g) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= sigmoidf(z[i]);
+          }
           float rs = 1.f;
           if (p.w_post) {
-            sum[0] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (live && has[i / 4]) sum[0] = fmaf(y[i], y[i], sum[0]);
-            row_sum(sum, sh, ph, s.tpr);
+            row_sum(sum, sh, ph, rw);
             rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
             if (p.rstd_post && live && lt == 0) p.rstd_post[row] = rs;
           }
-          float w[8], a[8];
-          load_vec(w, p.w_post, e, has);
-          load_vec(a, p.alpha, e, has);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float u = y[i] * rs * w[i] * a[i];
-            if (has_g) u *= sigmoidf(z[i]);
-            r[i] += u;
-          }
+          for (int i = 0; i < 8; ++i) r[i] = fmaf(y[i], rs, r[i]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<RT*>(p.r_out) + row * s.C + e[k], r + 4 * k);
+              store4(reinterpret_cast<RT*>(p.r_out) + o + e[k], r + 4 * k);
         }
         if (p.n) {
           sum[0] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (live && has[i / 4]) sum[0] = fmaf(r[i], r[i], sum[0]);
-          row_sum(sum, sh, ph, s.tpr);
+          for (int i = 0; i < 8; ++i) sum[0] = fmaf(r[i], r[i], sum[0]);
+          row_sum(sum, sh, ph, rw);
           const float rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
           if (p.rstd_pre && live && lt == 0) p.rstd_pre[row] = rs;
           float w[8];
-          load_vec(w, p.w_pre, e, has);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] *= r[i] * rs;
+          for (int i = 0; i < 8; ++i) w[i] = r[i] * rs * wp[i];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<YT*>(p.n) + row * s.C + e[k], w + 4 * k);
+              store4(reinterpret_cast<YT*>(p.n) + o + e[k], w + 4 * k);
         }
       });
 }
@@ -276,7 +290,7 @@ struct NormBwdParams {
   void* dr;
   void* dy;
   void* dgate;
-  float* part;  // [3][grid][C]: column sums of dw_pre, dw_post, dalpha
+  float* part;  // [2][grid][C]: column sums of dn x and g s yh
   NormShape s;
 };
 
@@ -290,11 +304,18 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
   const bool has[2] = {e[0] < s.C, e[1] < s.C};
   const bool has_n = p.in.t[0].p != nullptr, has_d = p.in.t[2].p != nullptr, has_y = p.in.t[3].p != nullptr,
              has_g = p.in.t[4].p != nullptr;
+  const RowWarps rw(s.tpr);
   norm_setup<RING>(sh, s);
-  float a_pre[8], a_post[8], a_al[8], dn[8], x[8], g[8], yh[8], z[8];
+  float wp[8], c[8];  // w_pre, w_post alpha
+  load_vec(c, p.w_post, e, has);
+  load_vec(wp, p.alpha, e, has);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a_pre[i] = a_post[i] = a_al[i] = 0.f;
-  float rs = 0.f, rsy = 1.f, rs_next = 0.f, rsy_next = 1.f;
+  for (int i = 0; i < 8; ++i) c[i] *= wp[i];
+  load_vec(wp, p.w_pre, e, has);
+  float a_pre[8], a_post[8], dn[8], x[8], g[8], yh[8], z[8];  // elements that the row does not have stay zero
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a_pre[i] = a_post[i] = dn[i] = x[i] = g[i] = yh[i] = z[i] = 0.f;
+  float rs_next = 0.f, rsy_next = 1.f;
   auto stats = [&](int64_t row) {  // a row's factors, read one group ahead
     if (row >= s.rows) return;
     if (has_n) rs_next = p.rstd_pre[row];
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
   int ph = 0;
   norm_walk<RING>(
       p.in, s, sh, sm + kNormHead,
-      [&](int64_t, auto at) {
+      [&](auto at) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
@@ -318,76 +339,66 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         }
       },
       [&](int64_t row, bool live) {
-        rs = rs_next, rsy = rsy_next;
+        // a thread without a row must add nothing to the column sums
+        const float rs = live ? rs_next : 0.f, rsy = live ? rsy_next : 0.f;
         stats(row + (int64_t)gridDim.x * s.rpb);
-        if (!live) rs = 0.f, rsy = 0.f;
-        float w[8], c[8], sum[3] = {0.f, 0.f, 0.f};
+        if (!live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = live && has[i / 4];
-          if (!in || !has_n) dn[i] = x[i] = 0.f;
-          if (!in || !has_d) g[i] = 0.f;
-          if (!in || !has_y) yh[i] = 0.f;
-          if (!in || !has_g) z[i] = 0.f;
+          for (int i = 0; i < 8; ++i) dn[i] = x[i] = g[i] = yh[i] = 0.f;
         }
+        if (!has_d) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = 0.f;
+        }
+        const int64_t o = row * s.C;
+        float sum[3] = {0.f, 0.f, 0.f};
         if (has_n) {
-          load_vec(w, p.w_pre, e, has);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             x[i] *= rs;
             a_pre[i] = fmaf(dn[i], x[i], a_pre[i]);
-            dn[i] *= w[i];
+            dn[i] *= wp[i];
             sum[0] = fmaf(dn[i], x[i], sum[0]);
             g[i] = fmaf(rs, dn[i], g[i]);
           }
         }
-        float sg[8];
         if (has_y) {
-          load_vec(w, p.w_post, e, has);
-          load_vec(c, p.alpha, e, has);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            sg[i] = has_g ? sigmoidf(z[i]) : 1.f;
+            z[i] = has_g ? sigmoidf(z[i]) : 1.f;
             yh[i] *= rsy;
-          }
-          if (p.w_post) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float ci = c[i] * sg[i] * w[i] * yh[i];
-              sum[1] = fmaf(ci, g[i], sum[1]);
-              sum[2] = fmaf(ci, x[i], sum[2]);
-            }
+            const float ci = c[i] * z[i] * yh[i];
+            sum[1] = fmaf(ci, g[i], sum[1]);
+            sum[2] = fmaf(ci, x[i], sum[2]);
           }
         }
-        if (has_n || p.w_post) row_sum(sum, sh, ph, s.tpr);
+        if (has_n || p.w_post) row_sum(sum, sh, ph, rw);
         const float m1 = rs * sum[0] * s.inv_c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = fmaf(-m1, x[i], g[i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-            store4(reinterpret_cast<RT*>(p.dr) + row * s.C + e[k], g + 4 * k);
+            store4(reinterpret_cast<RT*>(p.dr) + o + e[k], g + 4 * k);
         if (has_y) {
-          const float m2 = p.w_post ? fmaf(-m1, sum[2], sum[1]) * s.inv_c : 0.f;
+          const float m2 = p.w_post ? rsy * fmaf(-m1, sum[2], sum[1]) * s.inv_c : 0.f;
           float dz[8], dy[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float t = yh[i] * w[i], gs = g[i] * sg[i], dt = c[i] * gs;
-            a_al[i] = fmaf(gs, t, a_al[i]);
-            a_post[i] = fmaf(dt, yh[i], a_post[i]);
-            dz[i] = dt * t * (1.f - sg[i]);
-            dy[i] = rsy * (dt * w[i] - yh[i] * m2);
+            const float gs = g[i] * z[i], dt = gs * c[i];
+            a_post[i] = fmaf(gs, yh[i], a_post[i]);
+            dz[i] = dt * yh[i] * (1.f - z[i]);
+            dy[i] = fmaf(rsy, dt, -yh[i] * m2);
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C)) {
-              store4(reinterpret_cast<YT*>(p.dy) + row * s.C + e[k], dy + 4 * k);
-              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + row * s.C + e[k], dz + 4 * k);
+              store4(reinterpret_cast<YT*>(p.dy) + o + e[k], dy + 4 * k);
+              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + o + e[k], dz + 4 * k);
             }
         }
       });
   // this block's column sums: the row slots of a group added in order, then written once
-  const int64_t plane = (int64_t)gridDim.x * s.C;
   float* mine = p.part + (int64_t)blockIdx.x * s.C;
   float* acc = reinterpret_cast<float*>(sm + kNormHead);  // [rpb][C]
   auto put = [&](const float (&a)[8], float* dst) {
@@ -414,21 +425,21 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
     }
   };
   if (has_n) put(a_pre, mine);
-  if (p.w_post) put(a_post, mine + plane);
-  if (p.alpha) put(a_al, mine + 2 * plane);
+  if (p.w_post || p.alpha) put(a_post, mine + (int64_t)gridDim.x * s.C);
 }
 
 // Adds the blocks' column sums: 8 threads x 4 columns by 32 slices of blocks,
-// the slices then added in order.
+// the slices then added in order.  Plane 0 is dw_pre, plane 1 the sums S of
+// dw_post = alpha S and dalpha = w_post S.
 __global__ void __launch_bounds__(256) block_norm_cols_kernel(const float* __restrict__ part, float* dw_pre,
-                                                              float* dw_post, float* dalpha, int nblk, int C) {
+                                                              float* dw_post, float* dalpha, const float* w_post,
+                                                              const float* alpha, int nblk, int C) {
   __shared__ float4 sums[32][8];
-  float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dalpha;
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
   const int col = blockIdx.x * 32 + 4 * tx;
   pdl_launch_dependents();
   pdl_wait();
-  if (!out) return;
+  if (blockIdx.y == 0 ? !dw_pre : !dw_post && !dalpha) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < C) {
     const float* src = part + (int64_t)blockIdx.y * nblk * C + col;
@@ -446,13 +457,22 @@ __global__ void __launch_bounds__(256) block_norm_cols_kernel(const float* __res
       const float4 v = sums[s][tx];
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
-    *reinterpret_cast<float4*>(out + col) = a;
+    auto put = [&](float* out, const float* by) {
+      float4 f = by ? *reinterpret_cast<const float4*>(by + col) : make_float4(1.f, 1.f, 1.f, 1.f);
+      *reinterpret_cast<float4*>(out + col) = make_float4(a.x * f.x, a.y * f.y, a.z * f.z, a.w * f.w);
+    };
+    if (blockIdx.y == 0) {
+      put(dw_pre, nullptr);
+    } else {
+      if (dw_post) put(dw_post, alpha);
+      if (dalpha) put(dalpha, w_post);
+    }
   }
 }
 
 // ------------------------------------------------------------------ launchers
 // Threads an SM holds (forward 1024, at 64 registers; backward 512, whose
-// column sums take 24 more each); the stages then take the shared memory.
+// column sums and gradients take more); the stages then take the shared memory.
 constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
 constexpr int kNormSmem = 200 * 1024;
 
@@ -555,7 +575,7 @@ size_t block_norm_bwd_workspace(int64_t rows, int64_t C) {
   int tpr, rpb;
   norm_rows(C, tpr, rpb);
   const int64_t most = (int64_t)sm_count() * norm_blocks_per_sm(C, kBwdThreadsPerSm, 0);
-  return (size_t)std::min<int64_t>((rows + rpb - 1) / rpb, most) * 3 * (size_t)C * sizeof(float);
+  return (size_t)std::min<int64_t>((rows + rpb - 1) / rpb, most) * 2 * (size_t)C * sizeof(float);
 }
 
 int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t s) {
@@ -580,8 +600,8 @@ int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t s) {
   else if (yb) rc = norm_bwd_t<float, __nv_bfloat16>(c, p, s);
   else rc = norm_bwd_t<float, float>(c, p, s);
   if (rc != SAMBA_OK || !(a.dn || a.w_post || a.alpha)) return rc;
-  const cudaError_t e = launch_pdl(block_norm_cols_kernel, dim3((C + 31) / 32, 3), dim3(256), 0, s, (const float*)p.part,
-                                   a.dn ? a.dw_pre : nullptr, a.dw_post, a.dalpha, c.grid, C);
+  const cudaError_t e = launch_pdl(block_norm_cols_kernel, dim3((C + 31) / 32, 2), dim3(256), 0, s, (const float*)p.part,
+                                   a.dn ? a.dw_pre : nullptr, a.dw_post, a.dalpha, a.w_post, a.alpha, c.grid, C);
   if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return check_launch(who);
 }
