@@ -94,10 +94,10 @@ struct PagedCfg {
   static constexpr int WARPS = 4;
   static constexpr int ROWS = 8 * NT;                 // query rows a block
   static constexpr int RING = WARPS * STG * STAGE;
-  static constexpr int MERGE = WARPS * ROWS * HD * 4 + 2 * WARPS * ROWS * 4;
+  // the warps' results, then the block's: [WARPS + 1][ROWS][HD] and their maxima and sums
+  static constexpr int MERGE = (WARPS + 1) * ROWS * (HD + 2) * 4;
   static constexpr int BAR_OFF = RING > MERGE ? RING : (MERGE + 127) / 128 * 128;
-  static constexpr int TAB_OFF = BAR_OFF + 128;       // then the block's pages: number, scales
-  static constexpr int MAXCTA = 228 * 1024 / (TAB_OFF + 3 * 1024);  // blocks an SM holds by shared memory, about
+  static constexpr int TAB_OFF = BAR_OFF + 128;       // then the block's pages: scales, numbers
 };
 
 // Byte offset of 16-byte chunk c of row r in a stage matrix, as the tensor
@@ -129,7 +129,7 @@ __device__ __forceinline__ int slot_of(int c) {
 struct PagedParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
-  float* ws;           // [batch][max_q][Hq][nsplit][HD + 2] partial results, or null
+  float* ws;           // [batch][max_q][Hq][npart][HD + 2] partial results, or null
   const float* k_scale;
   const float* v_scale;
   samba_paged_batch batch;
@@ -137,7 +137,8 @@ struct PagedParams {
   int64_t window;
   int Hq, Hkv, group, page_shift;
   int ntile;           // row tiles a sequence
-  int nsplit, chunk;   // splits a row tile, positions a split (a multiple of 128)
+  int nsplit, chunk;   // splits a row tile, positions a split at most (a multiple of 32)
+  int cluster, npart;  // splits a cluster joins, results that leaves
   int ctab;            // pages a split can touch
   float scale_log2;
 };
@@ -166,6 +167,18 @@ __device__ __forceinline__ TileSpan tile_span(const PagedParams& p, int b, int t
   return t;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A float of another block of the cluster: `p` is this block's address of it.
+__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 template <int HD, bool KV8, int NT>
 __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant__ CUtensorMap map_k,
                                                           const __grid_constant__ CUtensorMap map_v,
@@ -176,8 +189,11 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::BAR_OFF);  // [WARPS][STG]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + Cfg::WARPS * STG);
-  int* tab = reinterpret_cast<int*>(sm + Cfg::TAB_OFF);             // [ctab] page numbers (num_pages: none)
-  float2* sct = reinterpret_cast<float2*>(tab + (p.ctab + 1) / 2 * 2);  // [ctab] key scale, value scale exponent
+  float4* sct = reinterpret_cast<float4*>(sm + Cfg::TAB_OFF);  // [ctab] key scale, value scale 2^e: e, 2^-e
+  int* tab = reinterpret_cast<int*>(sct + (KV8 ? p.ctab : 0));  // [ctab] page numbers (num_pages: none)
+  float* Ow = reinterpret_cast<float*>(sm);                    // after the ring's last use: [WARPS + 1][ROWS][HD]
+  float* wm = Ow + (Cfg::WARPS + 1) * ROWS * HD;               // [WARPS + 1][ROWS] maxima
+  float* wl = wm + (Cfg::WARPS + 1) * ROWS;                    // sums
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int split = blockIdx.x % p.nsplit, tile = blockIdx.x / p.nsplit % p.ntile, b = blockIdx.x / p.nsplit / p.ntile;
   const int g = blockIdx.y, P = 1 << p.page_shift;
@@ -192,67 +208,62 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
   pdl_launch_dependents();
   pdl_wait();
   const TileSpan t = tile_span(p, b, tile, ROWS, P, split == 0 && tile == 0 && g == 0 && tid == 0);
-  // this block's positions: split s of the range that starts at a stage boundary
-  const int base = t.lo / 128 * 128;
-  const int64_t c0 = base + static_cast<int64_t>(split) * p.chunk;
+  if (t.nrow == 0) return;  // all blocks of the cluster
+  // this block's positions: its share of the range that starts at a stage boundary
+  const int base = t.lo / 32 * 32;
+  const int share = p.cluster == 1 ? p.chunk : min(p.chunk, ((t.hi - base + p.nsplit - 1) / p.nsplit + 31) / 32 * 32);
+  const int64_t c0 = base + static_cast<int64_t>(split) * share;
   const int c_lo = static_cast<int>(c0 < t.hi ? c0 : t.hi);
-  const int c_hi = static_cast<int>(c0 + p.chunk < t.hi ? c0 + p.chunk : t.hi);
+  const int c_hi = static_cast<int>(c0 + share < t.hi ? c0 + share : t.hi);
   const int nsub = (c_hi - c_lo + SW - 1) / SW;
-  if (nsub == 0) {
-    // nothing here: an empty partial (and nothing to write for a tile without rows)
-    if (p.nsplit > 1)
-      for (int r = tid; r < t.nrow; r += 128) {
-        const int rr = t.row0 + r, tok = rr / p.group, h = g * p.group + rr % p.group;
-        p.ws[((((int64_t)b * p.batch.max_q + tok) * p.Hq + h) * p.nsplit + split) * (HD + 2)] = -INFINITY;
-      }
-    return;
-  }
+  bool done = false;  // this block has a result
+  if (nsub > 0) {
   // the pages of [c_lo, c_hi): those with a visible position are looked up, the rest read as nothing
   const int pg0 = c_lo >> p.page_shift, npg = ((c_hi - 1) >> p.page_shift) - pg0 + 1;
-  for (int i = tid; i < npg; i += 128) {
+  int pg_first = static_cast<int>(p.num_pages);  // the thread's first page, whose scales are read below
+  for (int i = tid; i < p.ctab; i += 128) {
     int pg = static_cast<int>(p.num_pages);
-    float2 sc = make_float2(1.f, 0.f);
-    if (((pg0 + i + 1) << p.page_shift) > t.lo) {
+    if (i < npg && ((pg0 + i + 1) << p.page_shift) > t.lo) {
       const int v = p.batch.block_table[(int64_t)b * p.batch.max_pages + pg0 + i];
-      if (v >= 0 && v < p.num_pages) {
-        pg = v;
-        if constexpr (KV8) {
-          const int64_t at = (int64_t)v * p.Hkv + g;
-          sc = make_float2(exp2i(stored_exponent(p.k_scale[at])), static_cast<float>(stored_exponent(p.v_scale[at])));
-        }
-      } else {
-        report_batch();
-      }
+      if (v >= 0 && v < p.num_pages) pg = v;
+      else report_batch();
     }
     tab[i] = pg;
-    if constexpr (KV8) sct[i] = sc;
+    if (i == tid) pg_first = pg;
   }
   __syncthreads();
 
-  // One TMA box a page and panel, or a part of a page: min(P, SW) rows.
+  // A lane issues one box: K or V, a panel, min(P, SW) rows of a page.
   const int brows = P < SW ? P : SW;
   unsigned char* ring = sm + warp * (STG * Cfg::STAGE);
   uint64_t* mybar = bars + warp * STG;
-  auto issue = [&](int it) {  // one lane: the warp's it-th stage
-    const int j = c_lo + (warp + it * Cfg::WARPS) * SW;
-    unsigned char* Ks = ring + (it % STG) * Cfg::STAGE;
-    uint64_t* bar = &mybar[it % STG];
-    mbar_arrive_expect_tx(bar, Cfg::STAGE);
-    for (int r = 0; r < SW; r += brows) {
-      const int pi = ((j + r) >> p.page_shift) - pg0;
-      const int pg = pi < npg ? tab[pi] : static_cast<int>(p.num_pages);  // num_pages: past the pool, read as zeros
-      const int blk = pg * p.Hkv + g, row = (j + r) & (P - 1);
-#pragma unroll
-      for (int pn = 0; pn < Cfg::NPANEL; ++pn) {
-        const int dst = pn * SW * Cfg::RB + r * Cfg::RB;
-        tma_load_3d(Ks + dst, &map_k, bar, pn * Cfg::PE, row, blk);
-        tma_load_3d(Ks + Cfg::MAT + dst, &map_v, bar, pn * Cfg::PE, row, blk);
-      }
+  const int bx_row = lane / (2 * Cfg::NPANEL) * brows, bx_pn = (lane >> 1) % Cfg::NPANEL;
+  const bool bx_in = bx_row < SW;
+  const uint32_t bx_dst = (lane & 1) * Cfg::MAT + bx_pn * SW * Cfg::RB + bx_row * Cfg::RB;
+  const CUtensorMap* bx_map = (lane & 1) ? &map_v : &map_k;
+  auto issue = [&](int st, int j) {  // positions j .. of the warp's stage st
+    if (lane == 0) mbar_arrive_expect_tx(&mybar[st], Cfg::STAGE);
+    __syncwarp();
+    if (bx_in) {
+      const int pg = tab[((j + bx_row) >> p.page_shift) - pg0];  // num_pages: past the pool, read as zeros
+      tma_load_3d(ring + st * Cfg::STAGE + bx_dst, bx_map, &mybar[st], bx_pn * Cfg::PE, (j + bx_row) & (P - 1),
+                  pg * p.Hkv + g);
     }
   };
   const int mine = (nsub - warp + Cfg::WARPS - 1) / Cfg::WARPS;  // stages of this warp
-  if (lane == 0)
-    for (int it = 0; it < STG && it < mine; ++it) issue(it);
+  for (int i = 0; i < STG && i < mine; ++i) issue(i, c_lo + (warp + i * Cfg::WARPS) * SW);
+  if constexpr (KV8) {  // under the first copies
+    for (int i = tid; i < p.ctab; i += 128) {
+      const int pg = i == tid ? pg_first : tab[i];
+      float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (pg < p.num_pages) {
+        const int64_t at = (int64_t)pg * p.Hkv + g;
+        const int ke = stored_exponent(p.k_scale[at]), ve = stored_exponent(p.v_scale[at]);
+        sc = make_float4(exp2i(ke), static_cast<float>(ve), exp2i(-ve), 0.f);
+      }
+      sct[i] = sc;
+    }
+  }
 
   // Query fragments (the B operand): column gq of tile nt is query row 8 nt + gq.
   uint32_t qb[NT][NKS][2];
@@ -325,15 +336,30 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
     for (int i = 0; i < NMT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
   }
+  if constexpr (KV8) __syncthreads();  // the scales are there
+  // A thread's places in a stage: rows 8 apart share the swizzle, so only the
+  // first is worked out.
+  uint32_t koff, voff[2];
+  if constexpr (KV8) {
+    const int r = slot_of<HD>(gq);
+    koff = HD >= 64   ? tile_off<Cfg>(r, tq)
+           : HD == 32 ? tile_off<Cfg>(r, tq >> 1) + 8 * (tq & 1)
+                      : tile_off<Cfg>(r, 0) + 4 * tq;
+    constexpr int NB = HD / 8;
+    for (int e = 0; e < 2; ++e) voff[e] = tile_off<Cfg>(slot_of<HD>(2 * tq + e), NB * gq / 16) + (NB * gq) % 16;
+  } else {
+    koff = tile_off<Cfg>(lane & 15, lane >> 4);
+    voff[0] = tile_off<Cfg>((lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1);
+    voff[1] = 0;
+  }
   bool ok = true;
-  int it = 0;
-  for (; it < mine; ++it) {
-    ok = __all_sync(0xffffffffu, mbar_wait(&mybar[it % STG], (it / STG) & 1, abort_flag));
+  int it = 0, st = 0, j0 = c_lo + warp * SW;
+  uint32_t ph = 0;
+  for (; it < mine; ++it, j0 += Cfg::WARPS * SW) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&mybar[st], ph, abort_flag));
     if (!ok) break;
-    const unsigned char* Ks = ring + (it % STG) * Cfg::STAGE;
-    const unsigned char* Vs = Ks + Cfg::MAT;
-    const uint32_t ka = smem_u32(Ks), va = smem_u32(Vs);
-    const int j0 = c_lo + (warp + it * Cfg::WARPS) * SW;
+    const unsigned char* Ks = ring + st * Cfg::STAGE + koff;
+    const unsigned char* Vs = ring + st * Cfg::STAGE + Cfg::MAT;
     const bool edge = j0 < full_lo || j0 + SW > full_hi;
     // scores: S^T[position, row]; accumulator rows gq and gq + 8 of group u
     float s[NT][NG][4];
@@ -343,25 +369,27 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][u][0] = s[nt][u][1] = s[nt][u][2] = s[nt][u][3] = 0.f;
       if constexpr (KV8) {
-        const int ra = 16 * u + slot_of<HD>(gq), rb = ra + 8;
         constexpr int NB = HD >= 64 ? 16 : HD / 4;       // bytes a thread reads of each 64 (or all)
         constexpr int NH = HD >= 64 ? HD / 64 : 1;
         uint32_t wa[NH][NB / 4], wb[NH][NB / 4];
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
+          // (the second 64 elements: the chunk's bit 2, flipped)
+          const unsigned char* pa = hf == 0 ? Ks : ring + st * Cfg::STAGE + (koff ^ 64u);
+          pa += 16 * u * Cfg::RB;
           if constexpr (NB == 16) {
-            const uint4 x = *reinterpret_cast<const uint4*>(Ks + tile_off<Cfg>(ra, 4 * hf + tq));
-            const uint4 y = *reinterpret_cast<const uint4*>(Ks + tile_off<Cfg>(rb, 4 * hf + tq));
+            const uint4 x = *reinterpret_cast<const uint4*>(pa);
+            const uint4 y = *reinterpret_cast<const uint4*>(pa + 8 * Cfg::RB);
             wa[hf][0] = x.x, wa[hf][1] = x.y, wa[hf][2] = x.z, wa[hf][3] = x.w;
             wb[hf][0] = y.x, wb[hf][1] = y.y, wb[hf][2] = y.z, wb[hf][3] = y.w;
           } else if constexpr (NB == 8) {
-            const uint2 x = *reinterpret_cast<const uint2*>(Ks + tile_off<Cfg>(ra, tq >> 1) + 8 * (tq & 1));
-            const uint2 y = *reinterpret_cast<const uint2*>(Ks + tile_off<Cfg>(rb, tq >> 1) + 8 * (tq & 1));
+            const uint2 x = *reinterpret_cast<const uint2*>(pa);
+            const uint2 y = *reinterpret_cast<const uint2*>(pa + 8 * Cfg::RB);
             wa[hf][0] = x.x, wa[hf][1] = x.y;
             wb[hf][0] = y.x, wb[hf][1] = y.y;
           } else {
-            wa[hf][0] = *reinterpret_cast<const uint32_t*>(Ks + tile_off<Cfg>(ra, 0) + 4 * tq);
-            wb[hf][0] = *reinterpret_cast<const uint32_t*>(Ks + tile_off<Cfg>(rb, 0) + 4 * tq);
+            wa[hf][0] = *reinterpret_cast<const uint32_t*>(pa);
+            wb[hf][0] = *reinterpret_cast<const uint32_t*>(pa + 8 * Cfg::RB);
           }
         }
 #pragma unroll
@@ -372,10 +400,9 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
         }
-        const int pi = ((j0 + 16 * u) >> p.page_shift) - pg0;
-        const float2 sc = pi < npg ? sct[pi] : make_float2(1.f, 0.f);
+        const float4 sc = sct[((j0 + 16 * u) >> p.page_shift) - pg0];
         kv_e[u] = sc.y;
-        inv_v[u] = exp2i(-static_cast<int>(sc.y));
+        inv_v[u] = sc.z;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -384,7 +411,8 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
         for (int ks = 0; ks < NKS; ++ks) {
           uint32_t a[4];
-          ldsm4(a, ka + tile_off<Cfg>(16 * u + (lane & 15), 2 * ks + (lane >> 4)));
+          constexpr int CPR = Cfg::RB / 16;
+          ldsm4(a, (smem_u32(Ks) ^ (2 * ks % CPR * 16)) + 2 * ks / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_b16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
         }
@@ -431,12 +459,17 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
         }
       }
     }
+    float mref[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float m0 = mref[nt][0], m1 = mref[nt][1];
         const float x0 = exp2_ap(s[nt][u][0] - m0), x1 = exp2_ap(s[nt][u][1] - m1);
         const float x2 = exp2_ap(s[nt][u][2] - m0), x3 = exp2_ap(s[nt][u][3] - m1);
         if constexpr (KV8) {
@@ -458,8 +491,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
         uint32_t w[4][NB >= 4 ? NB / 4 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // positions 2 tq, 2 tq + 1 of rows 0-7, then of rows 8-15
-          const int r = 16 * u + (i >> 1) * 8 + slot_of<HD>(2 * tq + (i & 1));
-          const unsigned char* src = Vs + tile_off<Cfg>(r, NB * gq / 16) + (NB * gq) % 16;
+          const unsigned char* src = Vs + voff[i & 1] + (16 * u + (i >> 1) * 8) * Cfg::RB;
           if constexpr (NB == 16) {
             const uint4 x = *reinterpret_cast<const uint4*>(src);
             w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
@@ -472,7 +504,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
             w[i][0] = *reinterpret_cast<const uint16_t*>(src);
           }
           if (tail) {
-            const int j = j0 + r;
+            const int j = j0 + 16 * u + (i >> 1) * 8 + slot_of<HD>(2 * tq + (i & 1));
             if (j >= c_hi || j < t.lo) {
 #pragma unroll
               for (int x = 0; x < (NB >= 4 ? NB / 4 : 1); ++x) w[i][x] = 0u;
@@ -503,7 +535,8 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < NMT; ++i) {
           uint32_t a[4];  // matrices: positions 0-7 | 8-15 by elements 0-7 | 8-15 of step i
-          ldsm4_t(a, va + tile_off<Cfg>(16 * u + (lane >> 4) * 8 + (lane & 7), 2 * i + ((lane >> 3) & 1)));
+          constexpr int CPR = Cfg::RB / 16;
+          ldsm4_t(a, ((smem_u32(Vs) + voff[0]) ^ (2 * i % CPR * 16)) + 2 * i / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
           a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_b16_16816(o[nt][i], a, pb[nt][0], pb[nt][1]);
@@ -511,7 +544,8 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
       }
     }
     __syncwarp();  // the stage has been read
-    if (lane == 0 && it + STG < mine) issue(it + STG);
+    if (it + STG < mine) issue(st, j0 + STG * Cfg::WARPS * SW);
+    if (++st == STG) st = 0, ph ^= 1;
   }
   if (!ok && lane == 0) {  // copies still in flight after a wait that gave up
     volatile int never = 0;
@@ -526,10 +560,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
       for (int x = 4; x <= 16; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
 
   // merge the warps in shared memory: each scales its share to the common maximum
-  if (!__syncthreads_and(ok)) return;
-  float* Ow = reinterpret_cast<float*>(sm);  // [WARPS][ROWS][HD]
-  float* wm = Ow + Cfg::WARPS * ROWS * HD;   // [WARPS][ROWS]
-  float* wl = wm + Cfg::WARPS * ROWS;
+  done = __syncthreads_and(ok);
   if (gq == 0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -558,25 +589,65 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
       }
     }
   __syncthreads();
-  for (int i = tid; i < t.nrow * HD; i += 128) {
-    const int r = i / HD, d = i % HD;
-    const int rr = t.row0 + r, tok = rr / p.group, h = g * p.group + rr % p.group;
-    float M = -INFINITY;
+  }
+  // the block's result goes behind the warps'
+  float* Ob = Ow + Cfg::WARPS * ROWS * HD;
+  float* bm = wm + Cfg::WARPS * ROWS;
+  float* bl = wl + Cfg::WARPS * ROWS;
+  auto merged = [&](int i, float& M, float& L, float& acc) {
+    const int r = i / HD;
+    M = -INFINITY, L = acc = 0.f;
+    if (!done) return;
 #pragma unroll
     for (int w = 0; w < Cfg::WARPS; ++w) M = fmaxf(M, wm[w * ROWS + r]);
-    float L = 0.f, acc = 0.f;
 #pragma unroll
     for (int w = 0; w < Cfg::WARPS; ++w) {
       const float mw = wm[w * ROWS + r];
       L = fmaf(wl[w * ROWS + r], mw == M ? (M == -INFINITY ? 0.f : 1.f) : exp2_ap(mw - M), L);
-      acc += Ow[(w * ROWS + r) * HD + d];
+      acc += Ow[w * ROWS * HD + i];
     }
+  };
+  const int total = t.nrow * HD;
+  if (p.cluster > 1) {
+    for (int i = tid; i < total; i += 128) {
+      float M, L, acc;
+      merged(i, M, L, acc);
+      Ob[i] = acc;
+      if (i % HD == 0) bm[i / HD] = M, bl[i / HD] = L;
+    }
+    cluster_sync();
+  }
+  // each block of the cluster finishes a part of the rows' elements
+  const uint32_t rank = split % p.cluster;
+  for (int i = rank * 128 + tid; i < total; i += 128 * p.cluster) {
+    const int r = i / HD, d = i % HD;
+    float M, L, acc;
+    if (p.cluster == 1) {
+      merged(i, M, L, acc);
+    } else {
+      float cm[8], cl[8], ca[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < p.cluster) cm[c] = cluster_load(bm + r, c), cl[c] = cluster_load(bl + r, c), ca[c] = cluster_load(Ob + i, c);
+      M = -INFINITY, L = acc = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < p.cluster) M = fmaxf(M, cm[c]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < p.cluster) {
+          const float f = cm[c] == M ? (M == -INFINITY ? 0.f : 1.f) : exp2_ap(cm[c] - M);
+          L = fmaf(cl[c], f, L);
+          acc = fmaf(ca[c], f, acc);
+        }
+    }
+    const int rr = t.row0 + r, tok = rr / p.group, h = g * p.group + rr % p.group;
     const int64_t at = (int64_t)(t.seq_row0 + tok) * p.Hq + h;
     if (!SAMBA_CHECK(t.seq_row0 + tok < p.batch.rows && h < p.Hq && split < p.nsplit)) continue;
-    if (p.nsplit == 1) {
+    if (p.npart == 1) {
       p.o[at * HD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
     } else {
-      float* dst = p.ws + ((((int64_t)b * p.batch.max_q + tok) * p.Hq + h) * p.nsplit + split) * (HD + 2);
+      float* dst = p.ws + ((((int64_t)b * p.batch.max_q + tok) * p.Hq + h) * p.npart + split / p.cluster) * (HD + 2);
       dst[2 + d] = acc;
       if (d == 0) {
         dst[0] = M;
@@ -584,29 +655,31 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
       }
     }
   }
+  if (p.cluster > 1) cluster_sync();  // the others have read this block's result
 }
 
-// Adds the splits of each (row, head): one warp each, HD / 32 elements a lane.
+// Joins the partial results of each (row, head): a block each, its warps take
+// every fourth one, E = HD / 32 elements a lane.
 template <int HD>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p, int page_size) {
   constexpr int E = HD >= 32 ? HD / 32 : 1;
+  __shared__ float sm[4][32][E + 1], sl[4];
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const SeqSpan s = seq_span(p.batch, page_size, b, false);
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);  // row within the sequence times Hq, plus head
+  const int i = blockIdx.x;  // row within the sequence times Hq, plus head
   if (i >= s.n * p.Hq) return;
-  const int64_t at = (int64_t)s.row0 * p.Hq + i;
-  const float* src = p.ws + ((int64_t)b * p.batch.max_q * p.Hq + i) * p.nsplit * (HD + 2);
+  const float* src = p.ws + ((int64_t)b * p.batch.max_q * p.Hq + i) * p.npart * (HD + 2);
   float M = -INFINITY;
-  for (int k = lane; k < p.nsplit; k += 32) M = fmaxf(M, src[k * (HD + 2)]);
+  for (int k = lane; k < p.npart; k += 32) M = fmaxf(M, src[k * (HD + 2)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < p.nsplit; ++k) {
+  for (int k = warp; k < p.npart; k += 4) {
     const float* q = src + k * (HD + 2);
     const float mk = q[0];
     if (mk == -INFINITY) continue;  // an empty split wrote nothing else
@@ -614,13 +687,20 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
     L = fmaf(q[1], f, L);
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (HD >= 32 || lane < HD) acc[e] = fmaf(q[2 + E * lane + e], f, acc[e]);
+      if (HD >= 32 || lane < HD) acc[e] = fmaf(q[2 + 32 * e + lane], f, acc[e]);
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  if (!SAMBA_CHECK(s.row0 + i / p.Hq < p.batch.rows)) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (HD >= 32 || lane < HD) p.o[at * HD + E * lane + e] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < E; ++e) sm[warp][lane][e] = acc[e];
+  if (lane == 0) sl[warp] = L;
+  __syncthreads();
+  L = sl[0] + sl[1] + sl[2] + sl[3];
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t at = (int64_t)s.row0 * p.Hq + i;
+  if (!SAMBA_CHECK(s.row0 + i / p.Hq < p.batch.rows)) return;
+  for (int d = threadIdx.x; d < HD; d += 128) {
+    const int ln = d & 31, e = d >> 5;
+    p.o[at * HD + d] = __float2bfloat16_rn((sm[0][ln][e] + sm[1][ln][e] + sm[2][ln][e] + sm[3][ln][e]) * inv);
+  }
 }
 
 // ------------------------------------------------------------------ launcher
@@ -628,9 +708,15 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
 // its tiles of 16 rows each read the keys again.
 constexpr int64_t kFewRows = 64;
 
-// Positions a split: the range of one row tile over as many splits as fill
-// the SMs four blocks deep, at least 128 (a warp's 32) and at most 2048 (which bounds
-// the page table in shared memory and keeps a ragged batch balanced).
+// Splits of a row tile's positions: as many as the SMs hold at once (64
+// sequences of 2048 positions, 8 bits: two splits each 20.8 us, one 26.4), of at
+// least 128 positions (32 a warp) and at most kMaxChunk.  A sequence's length
+// is shared out evenly.  Up to eight splits make one cluster, whose blocks join
+// their results through shared memory (16 sequences of 2048: 11.0 us, 13.3 with
+// a second kernel); more leave one result a cluster for the second kernel.
+// Batches that fill the SMs several times over take splits of 2048 positions
+// without clusters, so that a block without positions leaves at once.
+constexpr int64_t kMaxChunk = 8192;
 static PagedPlan paged_plan(const samba_paged_attn_args& a) {
   PagedPlan pl;
   const int64_t group = a.heads_q / a.kv.heads_kv;
@@ -639,11 +725,12 @@ static PagedPlan paged_plan(const samba_paged_attn_args& a) {
   if (pl.chunk_kernel) {
     // one block an SM: key tiles are split while units leave SMs idle, at least four tiles each
     pl.nt = pl.chunk = 0;
+    pl.cluster = 1;
     pl.ntile = (int)((rows + 255) / 256);
     int64_t span = a.batch.max_kv;
     if (a.window > 0) span = std::min<int64_t>(span, a.window + 256 / group + 128);
     const int64_t units = (int64_t)pl.ntile * a.kv.heads_kv * std::max<int64_t>(1, a.batch.batch);
-    pl.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm_count() / units, span / 512));
+    pl.nsplit = pl.npart = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm_count() / units, span / 512));
     return pl;
   }
   pl.nt = rows <= 8 ? 1 : 2;
@@ -651,24 +738,56 @@ static PagedPlan paged_plan(const samba_paged_attn_args& a) {
   int64_t span = std::max<int64_t>(1, a.batch.max_kv);
   const int64_t toks = (8 * pl.nt + group - 1) / group;
   if (a.window > 0) span = std::min<int64_t>(span, a.window + toks);
-  span += 128;  // a tile's range starts at the multiple of 128 below
+  span += 32;  // a tile's range starts at the multiple of 32 below
   const int64_t tiles = (int64_t)pl.ntile * a.kv.heads_kv * a.batch.batch;
-  const int64_t want = std::max<int64_t>(1, 4 * (int64_t)sm_count() / std::max<int64_t>(1, tiles));
-  int64_t chunk = (span + want - 1) / want;
-  chunk = std::min<int64_t>(2048, std::max<int64_t>(128, (chunk + 127) / 128 * 128));
-  pl.chunk = (int)chunk;
-  pl.nsplit = (int)((span + chunk - 1) / chunk);
+  const int row_bytes = a.kv.head_dim * (a.kv.dtype == SAMBA_E4M3 ? 1 : 2);
+  const int64_t resident = row_bytes <= 64 ? 4 : 2;  // blocks an SM holds (their rings take 48 or 96 KB)
+  // (seven eighths of them: clusters do not fill the last ones)
+  const int64_t want = resident * sm_count() * 7 / 8 / std::max<int64_t>(1, tiles);
+  const int64_t least = (span + kMaxChunk - 1) / kMaxChunk, most = (span + 127) / 128;
+  int64_t n = std::max<int64_t>(1, std::min<int64_t>(most, want)), c = 1;
+  if (least > n || n == 1) {
+    n = (span + 2047) / 2048;
+  } else {
+    while (2 * c <= n && c < 8) c *= 2;
+    if (c < 8 && c < least) c *= 2;
+    n = std::max<int64_t>(n / c, (least + c - 1) / c) * c;
+  }
+  pl.cluster = (int)c;
+  pl.nsplit = (int)n;
+  pl.npart = pl.nsplit / pl.cluster;
+  pl.chunk = (int)(((span + n - 1) / n + 31) / 32 * 32);
   return pl;
 }
 
 size_t paged_attn_workspace(const samba_paged_attn_args& a) {
   const PagedPlan pl = paged_plan(a);
-  if (pl.nsplit <= 1) return 0;
+  if (pl.npart <= 1) return 0;
   uint64_t n = 0;
   if (__builtin_mul_overflow((uint64_t)a.batch.batch, (uint64_t)a.batch.max_q, &n) ||
-      __builtin_mul_overflow(n, (uint64_t)a.heads_q, &n) || __builtin_mul_overflow(n, (uint64_t)pl.nsplit, &n) || __builtin_mul_overflow(n, (uint64_t)(a.kv.head_dim + 2) * 4, &n))
+      __builtin_mul_overflow(n, (uint64_t)a.heads_q, &n) || __builtin_mul_overflow(n, (uint64_t)pl.npart, &n) || __builtin_mul_overflow(n, (uint64_t)(a.kv.head_dim + 2) * 4, &n))
     return SIZE_MAX;
   return (size_t)n;
+}
+
+// launch_pdl of pdl.cuh with `cluster` blocks along x in a cluster.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem, cudaStream_t s,
+                                      Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int HD, bool KV8, int NT>
@@ -676,9 +795,9 @@ static int paged_go(const samba_paged_attn_args& a, const PagedPlan& pl, PagedPa
   using Cfg = PagedCfg<HD, KV8, NT>;
   auto kern = paged_split_kernel<HD, KV8, NT>;
   const int P = a.kv.page_size;
-  p.ctab = pl.chunk / P + 1;
-  const int smem = Cfg::TAB_OFF + (p.ctab + 1) * 4 + p.ctab * 8 + 1024 + 16;
-  constexpr int kMax = Cfg::TAB_OFF + (2048 / 16 + 2) * 12 + 1024 + 64;
+  p.ctab = pl.chunk / P + 2;
+  const int smem = Cfg::TAB_OFF + p.ctab * (KV8 ? 20 : 4) + 1024;
+  constexpr int kMax = Cfg::TAB_OFF + ((kMaxChunk + 32) / 16 + 2) * 20 + 1024;
   static_assert(kMax <= 227 * 1024, "shared memory");
   static_assert(Cfg::WARPS * Cfg::STG * 8 + 4 <= 128, "barrier block");
   static PerDeviceOnce attr;
@@ -704,7 +823,7 @@ static int paged_go(const samba_paged_attn_args& a, const PagedPlan& pl, PagedPa
   if (rc) return rc;
   const int64_t gx = a.batch.batch * pl.ntile * pl.nsplit;
   if (gx > INT32_MAX) return fail(SAMBA_ERR_UNSUPPORTED, "samba_paged_attn: too many rows");
-  const cudaError_t e = launch_pdl(kern, dim3((unsigned)gx, a.kv.heads_kv), dim3(128), smem, s, mk, mv, p);
+  const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)gx, a.kv.heads_kv), dim3(128), pl.cluster, smem, s, mk, mv, p);
   if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "samba_paged_attn: launch failed: %s", cudaGetErrorString(e));
   return check_launch("samba_paged_attn");
 }
@@ -716,8 +835,8 @@ static int paged_hd(const samba_paged_attn_args& a, const PagedPlan& pl, PagedPa
   if (pl.chunk_kernel) {}  // its splits are there already
   else if (pl.nt == 1) rc = kv8 ? paged_go<HD, true, 1>(a, pl, p, s) : paged_go<HD, false, 1>(a, pl, p, s);
   else rc = kv8 ? paged_go<HD, true, 2>(a, pl, p, s) : paged_go<HD, false, 2>(a, pl, p, s);
-  if (rc != SAMBA_OK || pl.nsplit == 1) return rc;
-  const int64_t cx = (a.batch.max_q * a.heads_q + 3) / 4;
+  if (rc != SAMBA_OK || pl.npart == 1) return rc;
+  const int64_t cx = a.batch.max_q * a.heads_q;
   const cudaError_t e = launch_pdl(paged_combine_kernel<HD>, dim3((unsigned)cx, (unsigned)a.batch.batch), dim3(128), 0, s, p,
                                    (int)a.kv.page_size);
   if (e != cudaSuccess) return fail(SAMBA_ERR_CUDA, "samba_paged_attn: launch failed: %s", cudaGetErrorString(e));
@@ -729,7 +848,7 @@ int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t s) {
   const PagedPlan pl = paged_plan(a);
   if (pl.chunk_kernel) {
     const int rc = launch_paged_chunk(a, pl, s);
-    if (rc != SAMBA_OK || pl.nsplit == 1) return rc;
+    if (rc != SAMBA_OK || pl.npart == 1) return rc;
   }
   PagedParams p;
   p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
@@ -747,6 +866,8 @@ int launch_paged_attn(const samba_paged_attn_args& a, cudaStream_t s) {
   p.ntile = pl.ntile;
   p.nsplit = pl.nsplit;
   p.chunk = pl.chunk;
+  p.cluster = pl.cluster;
+  p.npart = pl.npart;
   p.scale_log2 = paged_scale_log2(a);
   switch (a.kv.head_dim) {
     case 16: return paged_hd<16>(a, pl, p, s);

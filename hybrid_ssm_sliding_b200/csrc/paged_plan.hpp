@@ -11,7 +11,8 @@ struct PagedPlan {
   bool chunk_kernel;  // paged_chunk.cu (many rows a kv head) or paged_attn.cu
   int nt;             // paged_attn.cu: 8-row tiles of queries a block
   int ntile;          // row tiles (paged_chunk.cu: pairs of 128 rows) a sequence may have
-  int nsplit, chunk;  // splits a row tile; positions a split (paged_attn.cu)
+  int nsplit, chunk;  // splits a row tile; positions a split at most (paged_attn.cu)
+  int cluster, npart; // splits that a cluster joins; results that leaves
 };
 
 inline float paged_scale_log2(const samba_paged_attn_args& a) {
