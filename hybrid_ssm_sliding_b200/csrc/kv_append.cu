@@ -8,12 +8,17 @@
 // max |x| <= 448 s, so a block's largest value keeps the full three bits and
 // growing a scale only shifts the codes stored before.
 //
-// Bytes bound the call (q in and out, k and v in, the cache rows out).  A
-// thread block takes one (sequence, page) pair, which is what a scale
-// belongs to, and a share of the heads: the sines and cosines of its rows go
-// to shared memory once and serve all its heads.  Items of a sequence are
-// numbered from floor(q_start / page) + 2 b, which needs no prefix sum and
-// leaves each sequence at least as many numbers as it touches pages.
+// Bytes bound the call (q in and out, k and v in, the cache rows out).  Its
+// items are the (sequence, page) pairs, which is what a scale belongs to.  An
+// item has blocks for eight of its (matrix, kv head) blocks each, a warp one,
+// and blocks for a slice of its rows' queries each; a block brings the sines
+// and cosines of its rows to shared memory once for all its heads.  Items of a
+// sequence are numbered from floor(q_start / page) + 2 b, which needs no prefix
+// sum and leaves each sequence at least as many numbers as it touches pages.
+// A block of queries asks for its whole slice at once (a bulk copy a row, into
+// shared memory) before it works out the sines: the latency of loads, not the
+// arithmetic, is what kept a version with loads to registers at 93 us where
+// this one takes 77 (41k rows of 32 + 8 heads of 64).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -24,10 +29,13 @@ namespace samba {
 
 struct AppendParams {
   samba_kv_append_args a;
-  int nsplit;  // head shares an item is split into
+  // blocks an item for keys and values, for queries; slices of the query heads,
+  // heads and rows of one; bytes of the sines before a slice's queries
+  int nkv, nq, nhead, qheads, qrows, table_bytes;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256, kAppendBlocks = 3;  // three blocks an SM: 80 registers
+constexpr int kSliceBytes = 64 * 1024;                  // a slice of queries (48 KB, four blocks of 64 registers: 97 us)
 
 __device__ __forceinline__ void bf16x8_to_f32(uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -59,33 +67,43 @@ __device__ __forceinline__ PairChunk pair_chunk(int c, int rot, bool inter) {
   return {8 * c, rot / 2 + 8 * c, true};
 }
 
-// The pair chunk's two runs, rotated (x: run at lo, y: run at hi).
-__device__ __forceinline__ void load_rotated(const __nv_bfloat16* row, const PairChunk& pc, int c, bool inter,
-                                             const float* co, const float* si, float (&x)[8], float (&y)[8]) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(row + pc.lo), x);
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(row + pc.hi), y);
-  if (!pc.rot) return;
-  float cv[8], sv[8];
+// The pair chunk's two runs as loaded, the sines and cosines of its elements,
+// and the runs rotated (x: run at lo, y: run at hi).
+struct RawPair {
+  uint4 x, y;
+};
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ RawPair load_pair(const __nv_bfloat16* row, const PairChunk& pc) {
+  return {*reinterpret_cast<const uint4*>(row + pc.lo), *reinterpret_cast<const uint4*>(row + pc.hi)};
+}
+__device__ __forceinline__ void load_turn(Turn& t, const float* co, const float* si) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    *reinterpret_cast<float4*>(cv + 4 * i) = *reinterpret_cast<const float4*>(co + 8 * c + 4 * i);
-    *reinterpret_cast<float4*>(sv + 4 * i) = *reinterpret_cast<const float4*>(si + 8 * c + 4 * i);
+    *reinterpret_cast<float4*>(t.c + 4 * i) = *reinterpret_cast<const float4*>(co + 4 * i);
+    *reinterpret_cast<float4*>(t.s + 4 * i) = *reinterpret_cast<const float4*>(si + 4 * i);
   }
+}
+__device__ __forceinline__ void rotate(const RawPair& raw, bool rot, bool inter, const Turn& t, float (&x)[8], float (&y)[8]) {
+  bf16x8_to_f32(raw.x, x);
+  bf16x8_to_f32(raw.y, y);
+  if (!rot) return;
   if (inter) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float u = x[2 * i], w = x[2 * i + 1], u2 = y[2 * i], w2 = y[2 * i + 1];
-      x[2 * i] = u * cv[i] - w * sv[i];
-      x[2 * i + 1] = w * cv[i] + u * sv[i];
-      y[2 * i] = u2 * cv[4 + i] - w2 * sv[4 + i];
-      y[2 * i + 1] = w2 * cv[4 + i] + u2 * sv[4 + i];
+      x[2 * i] = u * t.c[i] - w * t.s[i];
+      x[2 * i + 1] = w * t.c[i] + u * t.s[i];
+      y[2 * i] = u2 * t.c[4 + i] - w2 * t.s[4 + i];
+      y[2 * i + 1] = w2 * t.c[4 + i] + u2 * t.s[4 + i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float u = x[i], w = y[i];
-      x[i] = u * cv[i] - w * sv[i];
-      y[i] = w * cv[i] + u * sv[i];
+      x[i] = u * t.c[i] - w * t.s[i];
+      y[i] = w * t.c[i] + u * t.s[i];
     }
   }
 }
@@ -95,14 +113,38 @@ __device__ __forceinline__ float finite_abs(float x) {  // |x|, 0 for NaN and in
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
+// body(r, pair) for the rows r = first, first + step .. below n, the loads of
+// two rows under way together.
+template <class Load, class Body>
+__device__ __forceinline__ void for_rows(int first, int step, int n, Load&& load, Body&& body) {
+  for (int r = first; r < n; r += 2 * step) {
+    RawPair raw[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (r + k * step < n) raw[k] = load(r + k * step);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (r + k * step < n) body(r + k * step, raw[k]);
+  }
+}
+
 template <bool KV8>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
-  extern __shared__ float table[];  // [n][rot / 2] cosines, then sines
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(128) float table[];  // [rows][rot / 2] cosines, then sines; a slice's queries
+  __shared__ int span[3];                          // q_start[b], q_start[b + 1], kv_len[b]
+  __shared__ uint64_t landed;                      // the slice's copies
+  __shared__ int abort_flag;
   const samba_kv_append_args& a = p.a;
   const int P = a.kv.page_size, d = a.kv.head_dim, Hkv = a.kv.heads_kv, Hq = a.heads_q, rot = a.rot_dim;
+  const int pshift = 31 - __clz(P), pcshift = 27 - __clz(d);  // log2 of P and of d / 16
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool inter = a.interleaved != 0;
-  const int item = blockIdx.x / p.nsplit, share = blockIdx.x % p.nsplit;
+  const int per_item = p.nkv + p.nq, item = blockIdx.x / per_item, part = blockIdx.x % per_item;
+  if (tid == 0) {
+    mbar_init(&landed, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
   // the sequence: the last one whose first item number is at most this one
@@ -110,127 +152,168 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
   int b = -1;
   for (int i0 = 0; i0 < B; i0 += kAppendThreads) {
     const int i = i0 + tid;
-    const bool below = i < B && static_cast<int64_t>(a.batch.q_start[i] / P) + 2 * i <= item;
-    b += __syncthreads_count(below);
-    if (blockIdx.x == 0 && i < B) seq_span(a.batch, P, i, true);  // one block reports what is out of range
+    int q0 = 0, q1 = 0, kv = 0;
+    if (i < B) q0 = a.batch.q_start[i], q1 = a.batch.q_start[i + 1], kv = a.batch.kv_len[i];
+    b += __syncthreads_count(i < B && static_cast<int64_t>(q0 / P) + 2 * i <= item);
+    if (i == b) span[0] = q0, span[1] = q1, span[2] = kv;
+    if (blockIdx.x == 0 && i < B) check_span(a.batch, P, q0, q1, kv, true);  // one block reports what is out of range
   }
   if (b < 0) return;
-  const int q0 = a.batch.q_start[b];
-  const int j = item - q0 / P - 2 * b;  // page of the sequence's new rows
-  const SeqSpan s = seq_span(a.batch, P, b, false);
+  __syncthreads();
+  const int j = item - span[0] / P - 2 * b;  // page of the sequence's new rows
+  const SeqSpan s = check_span(a.batch, P, span[0], span[1], span[2], false);
   if (s.n == 0) return;
-  const int first = s.kv - s.n;                       // position of the sequence's first new row
-  const int col = first / P + j;                      // block_table column
-  const int lo = j == 0 ? first : col * P;            // positions [lo, hi) of this item
-  const int hi = min(s.kv, (col + 1) * P);
-  const int n = hi - lo, off = lo - col * P, row0 = s.row0 + lo - first;
-  if (j < 0 || n <= 0) return;
-  const int page = a.batch.block_table[(int64_t)b * a.batch.max_pages + col];
-  const bool page_ok = page >= 0 && page < a.kv.num_pages;
-  if (!page_ok && tid == 0 && share == 0) report_batch();
-
-  const int half = rot / 2;
+  const int first = s.kv - s.n;                  // position of the sequence's first new row
+  const int col = (first >> pshift) + j;         // block_table column
+  const int lo = j == 0 ? first : col << pshift; // positions [lo, hi) of this item
+  const int hi = min(s.kv, (col + 1) << pshift);
+  if (j < 0 || hi <= lo) return;
+  const bool keys = part < p.nkv;                // this block's part: keys and values, or queries
+  const int row_lo = keys ? 0 : (part - p.nkv) / p.nhead * p.qrows;
+  const int n = keys ? hi - lo : min(hi - lo - row_lo, p.qrows);  // its rows of the item, from row_lo
+  if (n <= 0) return;
+  const int row0 = s.row0 + lo - first + row_lo;
+  const int half = rot / 2, PC = d >> 4;
   float* co = table;
   float* si = table + n * half;
-  for (int i = tid; i < n * half; i += kAppendThreads) {
-    const int r = i / half;
-    double turn = static_cast<double>(lo + r) * a.freqs[i - r * half] * 0.15915494309189535;  // 1 / (2 pi)
-    turn -= rint(turn);
-    sincospif(2.f * static_cast<float>(turn), si + i, co + i);
-  }
-  __syncthreads();
+  auto fill = [&]() {  // a lane a frequency, a warp every eighth row
+    for (int c = lane; c < half; c += 32) {
+      const double f = a.freqs[c] * 0.15915494309189535;  // turns a position: 1 / (2 pi)
+      for (int r = warp; r < n; r += kAppendThreads / 32) {
+        double turn = static_cast<double>(lo + row_lo + r) * f;
+        turn -= rint(turn);
+        sincospif(2.f * static_cast<float>(turn), si + r * half + c, co + r * half + c);
+      }
+    }
+    __syncthreads();
+  };
 
-  const int PC = d / 16;
-  // keys and values: one warp a (matrix, kv head)
-  if (page_ok) {
-    for (int u = share * (kAppendThreads / 32) + warp; u < 2 * Hkv; u += p.nsplit * (kAppendThreads / 32)) {
-      const bool is_v = u >= Hkv;
-      const int h = is_v ? u - Hkv : u;
-      const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + (int64_t)row0 * (is_v ? a.ldv : a.ldk) +
-                                 (int64_t)h * d;
-      const int64_t ld = is_v ? a.ldv : a.ldk;
-      const int64_t blk = ((int64_t)page * Hkv + h) * P;  // row of the (page, head) block
-      const int urot = is_v ? 0 : rot;
-      if constexpr (KV8) {
-        uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + blk * d;
-        float* scale = (is_v ? a.kv.v_scale : a.kv.k_scale) + (int64_t)page * Hkv + h;
-        float amax = 0.f;
-        for (int i = lane; i < n * PC; i += 32) {
-          const int r = i / PC, c = i - r * PC;
-          float x[8], y[8];
-          load_rotated(src + r * ld, pair_chunk(c, urot, inter), c, inter, co + r * half, si + r * half, x, y);
+  if (!keys) {
+    // Queries: a warp takes every eighth row of the slice (with few heads,
+    // several rows at a time), a lane the same chunk of every 32 / PC-th head.
+    const int h_lo = (part - p.nkv) % p.nhead * p.qheads, nh = min(p.qheads, Hq - h_lo), row_elems = nh * d;
+    __nv_bfloat16* in = reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(table) + p.table_bytes);
+    if (warp == 0) {
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)row0 * a.ldq + (int64_t)h_lo * d;
+      if (lane == 0) mbar_arrive_expect_tx(&landed, n * row_elems * 2);
+      __syncwarp();
+      for (int r = lane; r < n; r += 32) bulk_load(in + r * row_elems, q + r * a.ldq, row_elems * 2, &landed);
+    }
+    fill();
+    if (!mbar_wait(&landed, 0, &abort_flag)) {
+      volatile int never = 0;
+      if (tid == 0) mbar_wait(&landed, 0, &never);  // (copies still in flight)
+      return;
+    }
+    const int per_row = nh * PC, rp = per_row < 32 ? 32 / per_row : 1;
+    const int rsub = per_row < 32 ? lane / per_row : 0, k = per_row < 32 ? lane - rsub * per_row : lane;
+    const int c = k & (PC - 1), h0 = k >> pcshift, hstep = 32 >> pcshift;
+    const PairChunk pc = pair_chunk(c, rot, inter);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.q_out) + ((int64_t)row0 * Hq + h_lo) * d;
+    if (rsub >= rp) return;
+    for (int r = warp * rp + rsub; r < n; r += kAppendThreads / 32 * rp) {
+      Turn t;
+      if (pc.rot) load_turn(t, co + r * half + 8 * c, si + r * half + 8 * c);
+#pragma unroll 2
+      for (int h = h0; h < nh; h += hstep) {
+        float x[8], y[8];
+        rotate(load_pair(in + r * row_elems + h * d, pc), pc.rot, inter, t, x, y);
+        __nv_bfloat16* to = out + ((int64_t)r * Hq + h) * d;
+        if (!SAMBA_CHECK(row0 + r < a.batch.rows && h_lo + h < Hq)) continue;
+        *reinterpret_cast<uint4*>(to + pc.lo) = f32_to_bf16x8(x);
+        *reinterpret_cast<uint4*>(to + pc.hi) = f32_to_bf16x8(y);
+      }
+    }
+    return;
+  }
+  // keys and values: one warp a (matrix, kv head), keys first
+  const int page = a.batch.block_table[(int64_t)b * a.batch.max_pages + col];
+  if (page < 0 || page >= a.kv.num_pages) {
+    if (tid == 0 && part == 0) report_batch();
+    return;
+  }
+  const int off = lo - (col << pshift), u = part * (kAppendThreads / 32) + warp;
+  if (part * (kAppendThreads / 32) < Hkv) fill();
+  if (u >= 2 * Hkv) return;
+  const bool is_v = u >= Hkv;
+  const int h = is_v ? u - Hkv : u;
+  const int64_t ld = is_v ? a.ldv : a.ldk;
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + (int64_t)row0 * ld + (int64_t)h * d;
+  const int64_t blk = ((int64_t)page * Hkv + h) * P;  // row of the (page, head) block
+  // a lane takes the same chunk of every 32 / PC-th row
+  const int c = lane & (PC - 1), r0 = lane >> pcshift, rstep = 32 >> pcshift;
+  const PairChunk pc = pair_chunk(c, is_v ? 0 : rot, inter);
+  auto load = [&](int r) { return load_pair(src + r * ld, pc); };
+  auto turned = [&](int r, const RawPair& raw, float (&x)[8], float (&y)[8]) {
+    Turn t;
+    if (pc.rot) load_turn(t, co + r * half + 8 * c, si + r * half + 8 * c);
+    rotate(raw, pc.rot, inter, t, x, y);
+  };
+  if constexpr (KV8) {
+    uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + blk * d;
+    float* scale = (is_v ? a.kv.v_scale : a.kv.k_scale) + (int64_t)page * Hkv + h;
+    const float was_scale = off > 0 ? *scale : 0.f;
+    float amax = 0.f;  // of finite values; infinities are looked at again only where there are any
+    for (int finite = 0; finite < 2; ++finite) {
+      amax = 0.f;
+      for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
+        float x[8], y[8];
+        turned(r, raw, x, y);
+        if (finite) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(finite_abs(x[e]), finite_abs(y[e])));
+          for (int e = 0; e < 8; ++e) x[e] = finite_abs(x[e]), y[e] = finite_abs(y[e]);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int need = scale_exponent(amax);
-        int k = need;
-        if (off > 0) {  // the page holds earlier rows at its old scale
-          const int was = stored_exponent(*scale);
-          k = max(need, was);
-          if (k > was) {  // code * 2^(was - k), re-rounded
-            const float by = exp2i(max(was - k, -126));
-            uint4* old = reinterpret_cast<uint4*>(dst);
-            for (int i = lane; i < off * d / 16; i += 32) {
-              uint4 v = old[i];
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));  // (NaN is passed over)
+      });
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t l2 = e4m3x2_to_f16x2(w[e], false), h2 = e4m3x2_to_f16x2(w[e], true);
-                const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l2));
-                const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                w[e] = to_e4m3x4(fl.x * by, fl.y * by, fh.x * by, fh.y * by);
-              }
-              if (SAMBA_CHECK(i * 16 + 16 <= P * d)) old[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (amax <= 3.402823466e38f) break;
+    }
+    int k = scale_exponent(amax);
+    if (off > 0) {  // the page holds earlier rows at its old scale
+      const int was = stored_exponent(was_scale);
+      k = max(k, was);
+      if (k > was) {  // code * 2^(was - k), re-rounded
+        const float by = exp2i(was - k);
+        uint4* old = reinterpret_cast<uint4*>(dst);
+        for (int i = lane; i < off * d / 16; i += 32) {
+          uint4 v = old[i];
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t l2 = e4m3x2_to_f16x2(w[e], false), h2 = e4m3x2_to_f16x2(w[e], true);
+            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l2));
+            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            w[e] = to_e4m3x4(fl.x * by, fl.y * by, fh.x * by, fh.y * by);
           }
-        }
-        __syncwarp();  // every lane has read the old scale
-        if (lane == 0 && SAMBA_CHECK(page < a.kv.num_pages && h < Hkv)) *scale = exp2i(k);
-        const float inv = exp2i(-k);
-        for (int i = lane; i < n * PC; i += 32) {
-          const int r = i / PC, c = i - r * PC;
-          const PairChunk pc = pair_chunk(c, urot, inter);
-          float x[8], y[8];
-          load_rotated(src + r * ld, pc, c, inter, co + r * half, si + r * half, x, y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv, y[e] *= inv;
-          uint8_t* to = dst + (off + r) * d;
-          if (!SAMBA_CHECK(off + r < P)) continue;
-          *reinterpret_cast<uint2*>(to + pc.lo) = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
-          *reinterpret_cast<uint2*>(to + pc.hi) = make_uint2(to_e4m3x4(y[0], y[1], y[2], y[3]), to_e4m3x4(y[4], y[5], y[6], y[7]));
-        }
-      } else {
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.kv.v : a.kv.k) + blk * d;
-        for (int i = lane; i < n * PC; i += 32) {
-          const int r = i / PC, c = i - r * PC;
-          const PairChunk pc = pair_chunk(c, urot, inter);
-          float x[8], y[8];
-          load_rotated(src + r * ld, pc, c, inter, co + r * half, si + r * half, x, y);
-          __nv_bfloat16* to = dst + (off + r) * d;
-          if (!SAMBA_CHECK(off + r < P)) continue;
-          *reinterpret_cast<uint4*>(to + pc.lo) = f32_to_bf16x8(x);
-          *reinterpret_cast<uint4*>(to + pc.hi) = f32_to_bf16x8(y);
+          if (SAMBA_CHECK(i * 16 + 16 <= P * d)) old[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
-  }
-  // this share's queries
-  if (!a.q) return;
-  const int h0 = Hq * share / p.nsplit, nh = Hq * (share + 1) / p.nsplit - h0;
-  const int per_row = nh * PC;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)row0 * a.ldq + (int64_t)h0 * d;
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.q_out) + ((int64_t)row0 * Hq + h0) * d;
-  for (int i = tid; i < n * per_row; i += kAppendThreads) {
-    const int r = i / per_row, k = i - r * per_row, h = k / PC, c = k - h * PC;
-    const PairChunk pc = pair_chunk(c, rot, inter);
-    float x[8], y[8];
-    load_rotated(q + r * a.ldq + h * d, pc, c, inter, co + r * half, si + r * half, x, y);
-    __nv_bfloat16* to = out + ((int64_t)r * Hq + h) * d;
-    if (!SAMBA_CHECK(row0 + r < a.batch.rows && h0 + h < Hq)) continue;
-    *reinterpret_cast<uint4*>(to + pc.lo) = f32_to_bf16x8(x);
-    *reinterpret_cast<uint4*>(to + pc.hi) = f32_to_bf16x8(y);
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0 && SAMBA_CHECK(page < a.kv.num_pages && h < Hkv)) *scale = exp2i(k);
+    const float inv = exp2i(-k);
+    for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
+      float x[8], y[8];
+      turned(r, raw, x, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv, y[e] *= inv;
+      uint8_t* to = dst + (off + r) * d;
+      if (!SAMBA_CHECK(off + r < P)) return;
+      *reinterpret_cast<uint2*>(to + pc.lo) = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
+      *reinterpret_cast<uint2*>(to + pc.hi) = make_uint2(to_e4m3x4(y[0], y[1], y[2], y[3]), to_e4m3x4(y[4], y[5], y[6], y[7]));
+    });
+  } else {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.kv.v : a.kv.k) + blk * d;
+    for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
+      float x[8], y[8];
+      turned(r, raw, x, y);
+      __nv_bfloat16* to = dst + (off + r) * d;
+      if (!SAMBA_CHECK(off + r < P)) return;
+      *reinterpret_cast<uint4*>(to + pc.lo) = f32_to_bf16x8(x);
+      *reinterpret_cast<uint4*>(to + pc.hi) = f32_to_bf16x8(y);
+    });
   }
 }
 
@@ -249,18 +332,24 @@ static int kv_append_go(const AppendParams& p, unsigned grid, size_t smem, cudaS
 }
 
 int launch_kv_append(const samba_kv_append_args& a, cudaStream_t s) {
-  if (a.batch.batch == 0 || a.batch.rows == 0) return SAMBA_OK;
+  if (a.batch.batch == 0 || a.batch.rows == 0 || a.batch.max_q == 0) return SAMBA_OK;
   const int P = a.kv.page_size;
   AppendParams p;
   p.a = a;
-  // enough thread blocks for about four on each SM, at least two heads each
-  const int64_t items = a.batch.rows / P + a.batch.batch;
-  const int heads = std::max(a.q ? a.heads_q : 0, 2 * a.kv.heads_kv);
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((heads + 1) / 2, (4 * (int64_t)sm_count() + items - 1) / items));
-  const int64_t grid = (a.batch.rows / P + 2 * a.batch.batch) * p.nsplit;
+  const int page_rows = (int)std::min<int64_t>(P, a.batch.max_q), head_bytes = a.kv.head_dim * 2;
+  p.nkv = (2 * a.kv.heads_kv + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  // a slice: whole rows, or for very wide ones a row's share of the heads
+  p.qheads = std::min(std::max(1, a.heads_q), kSliceBytes / head_bytes);
+  p.nhead = a.q ? (a.heads_q + p.qheads - 1) / p.qheads : 1;
+  p.qrows = std::min(page_rows, std::max(1, kSliceBytes / (p.qheads * head_bytes)));
+  if (p.qrows > 8) p.qrows = p.qrows / 8 * 8;
+  p.nq = a.q ? (page_rows + p.qrows - 1) / p.qrows * p.nhead : 0;
+  const int64_t grid = (a.batch.rows / P + 2 * a.batch.batch) * ((int64_t)p.nkv + p.nq);
   if (grid > INT32_MAX) return fail(SAMBA_ERR_UNSUPPORTED, "samba_kv_append: too many rows");
   // a block's rows are those of one page, and of one sequence
-  const size_t smem = (size_t)std::min<int64_t>(P, a.batch.max_q) * a.rot_dim * sizeof(float);
+  p.table_bytes = (p.qrows * a.rot_dim * (int)sizeof(float) + 127) / 128 * 128;
+  const size_t smem = std::max<size_t>((size_t)page_rows * a.rot_dim * sizeof(float),
+                                       a.q ? p.table_bytes + (size_t)p.qrows * p.qheads * head_bytes : 0);
   return a.kv.dtype == SAMBA_E4M3 ? kv_append_go<true>(p, (unsigned)grid, smem, s)
                                   : kv_append_go<false>(p, (unsigned)grid, smem, s);
 }

@@ -15,10 +15,9 @@ struct SeqSpan {
   int row0, n, kv;
 };
 
-// Sequence b, checked against the call's sizes; n = 0 where it is out of range
-// (and reported, if `report`).
-__device__ __forceinline__ SeqSpan seq_span(const samba_paged_batch& bt, int page_size, int b, bool report) {
-  const int s0 = bt.q_start[b], s1 = bt.q_start[b + 1], kv = bt.kv_len[b];
+// A sequence's entries, checked against the call's sizes; n = 0 where they are
+// out of range (and reported, if `report`).
+__device__ __forceinline__ SeqSpan check_span(const samba_paged_batch& bt, int page_size, int s0, int s1, int kv, bool report) {
   SeqSpan s{s0, s1 - s0, kv};
   const int64_t n = static_cast<int64_t>(s1) - s0;
   if (s0 < 0 || n < 0 || s1 > bt.rows || n > bt.max_q || kv < n || kv > bt.max_kv || kv > bt.max_pages * page_size) {
@@ -26,6 +25,9 @@ __device__ __forceinline__ SeqSpan seq_span(const samba_paged_batch& bt, int pag
     s.n = 0;
   }
   return s;
+}
+__device__ __forceinline__ SeqSpan seq_span(const samba_paged_batch& bt, int page_size, int b, bool report) {
+  return check_span(bt, page_size, bt.q_start[b], bt.q_start[b + 1], bt.kv_len[b], report);
 }
 
 // Power of two 2^k as a float, k in [-126, 127].
