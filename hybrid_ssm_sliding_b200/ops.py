@@ -432,6 +432,13 @@ def _same(t, name, dtype, shape, dev):
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
 
 
+def _all_same(named, dev):
+    """_same for each (tensor or None, name, dtype, shape)."""
+    for t, name, dtype, shape in named:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _same(t, name, dtype, shape, dev)
+
+
 def _here(dev, stream):
     """A guard that makes device number ``dev`` current; refuses another device's stream."""
     if stream is not None and stream.device.index != dev:
@@ -632,10 +639,12 @@ def _norm_rows(r):
     """Checks the residual stream; returns its shape, rows, width, type's code and device."""
     if not isinstance(r, torch.Tensor) or r.dim() < 1:
         raise ValueError("r must be a [..., width] tensor")
-    _need(r, "r")
+    dev = r.get_device()
+    if dev < 0 or not r.is_contiguous():
+        _need(r, "r")
     shape = r.shape
     C = shape[-1]
-    return shape, r.numel() // C if C else 0, C, L.dtype_code(r), r.get_device()
+    return shape, r.numel() // C if C else 0, C, _norm_code(r.dtype), dev
 
 
 def _norm_code(dt):
@@ -667,22 +676,26 @@ def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, ep
     ycode = _norm_code(ydt)
     if w_pre is None and (n is not None or rstd_pre is not None):
         raise ValueError("n and rstd_pre go with w_pre")
-    for t, name, dt, sh in ((w_pre, "w_pre", f32, (C,)), (w_post, "w_post", f32, (C,)), (alpha, "alpha", f32, (C,)),
-                            (gate, "gate", ydt, shape), (r_out, "r_out", r.dtype, shape), (n, "n", ydt, shape),
-                            (rstd_pre, "rstd_pre", f32, (M,)), (rstd_post, "rstd_post", f32, (M,))):
-        if t is not None:
-            _same(t, name, dt, sh, dev)
+    vec = (C,)
+    _all_same(((w_pre, "w_pre", f32, vec), (w_post, "w_post", f32, vec), (alpha, "alpha", f32, vec),
+               (gate, "gate", ydt, shape)), dev)
+    if r_out is not None or n is not None or rstd_pre is not None or rstd_post is not None:
+        _all_same(((r_out, "r_out", r.dtype, shape), (n, "n", ydt, shape), (rstd_pre, "rstd_pre", f32, (M,)),
+                   (rstd_post, "rstd_post", f32, (M,))), dev)
     with _here(dev, stream):
         if y is not None and r_out is None:
             r_out = torch.empty_like(r)
             _lend(stream, r_out)
         if w_pre is not None and n is None:
-            n = torch.empty_like(r, dtype=ydt)
+            n = torch.empty_like(r, dtype=ydt) if y is None else torch.empty_like(y)
             _lend(stream, n)
         if M > 0:
-            p = L.ptr
-            a = L.BlockNormArgs(r.data_ptr(), p(y), p(w_pre), p(w_post), p(gate), p(alpha), p(r_out), p(n), p(rstd_pre),
-                                p(rstd_post), M, C, rcode, ycode, eps)
+            a = L.BlockNormArgs(
+                r.data_ptr(), None if y is None else y.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
+                None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(),
+                None if alpha is None else alpha.data_ptr(), None if r_out is None else r_out.data_ptr(),
+                None if n is None else n.data_ptr(), None if rstd_pre is None else rstd_pre.data_ptr(),
+                None if rstd_post is None else rstd_post.data_ptr(), M, C, rcode, ycode, eps)
             L.check(L.load().samba_block_norm_fwd(ctypes.byref(a), L.stream_handle(stream)))
     return (r if y is None else r_out), n
 
@@ -710,12 +723,10 @@ def block_norm_bwd(dn, r, w_pre=None, rstd_pre=None, dr_out=None, y=None, w_post
         raise ValueError("w_post needs rstd_post")
     ydt = y.dtype if y is not None else dn.dtype if dn is not None else rdt
     ycode = _norm_code(ydt)
-    for t, name, dt, sh in ((dn, "dn", ydt, shape), (dr_out, "dr_out", rdt, shape), (y, "y", ydt, shape),
-                            (gate, "gate", ydt, shape), (w_pre, "w_pre", f32, (C,)), (w_post, "w_post", f32, (C,)),
-                            (alpha, "alpha", f32, (C,)), (rstd_pre, "rstd_pre", f32, (M,)),
-                            (rstd_post, "rstd_post", f32, (M,))):
-        if t is not None:
-            _same(t, name, dt, sh, dev)
+    vec, rows = (C,), (M,)
+    _all_same(((dn, "dn", ydt, shape), (dr_out, "dr_out", rdt, shape), (y, "y", ydt, shape), (gate, "gate", ydt, shape),
+               (w_pre, "w_pre", f32, vec), (w_post, "w_post", f32, vec), (alpha, "alpha", f32, vec),
+               (rstd_pre, "rstd_pre", f32, rows), (rstd_post, "rstd_post", f32, rows)), dev)
     if workspace is not None:
         _same(workspace, "workspace", torch.uint8, workspace.shape, dev)
     with _here(dev, stream):
