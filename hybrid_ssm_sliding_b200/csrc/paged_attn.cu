@@ -47,6 +47,19 @@ __device__ __forceinline__ void mma_b16_16816(float (&c)[4], const uint32_t (&a)
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with C = 0.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_b16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t saddr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
   using Cfg = PagedCfg<HD, KV8, NT>;
   constexpr int SW = Cfg::SW, STG = Cfg::STG, NG = SW / 16, NMT = HD / 16, NKS = HD / 16, ROWS = Cfg::ROWS;
   extern __shared__ unsigned char sm_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);  // (an offset: still known as shared memory)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::BAR_OFF);  // [WARPS][STG]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + Cfg::WARPS * STG);
   float4* sct = reinterpret_cast<float4*>(sm + Cfg::TAB_OFF);  // [ctab] key scale, value scale 2^e: e, 2^-e
@@ -366,8 +379,6 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
     float kv_e[NG], inv_v[NG];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][u][0] = s[nt][u][1] = s[nt][u][2] = s[nt][u][3] = 0.f;
       if constexpr (KV8) {
         constexpr int NB = HD >= 64 ? 16 : HD / 4;       // bytes a thread reads of each 64 (or all)
         constexpr int NH = HD >= 64 ? HD / 64 : 1;
@@ -398,7 +409,10 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
           const uint32_t a[4] = {e4m3x2_to_f16x2(x, false), e4m3x2_to_f16x2(y, false), e4m3x2_to_f16x2(x, true),
                                  e4m3x2_to_f16x2(y, true)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (ks == 0) mma_f16_first(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+            else mma_f16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+          }
         }
         const float4 sc = sct[((j0 + 16 * u) >> p.page_shift) - pg0];
         kv_e[u] = sc.y;
@@ -414,7 +428,10 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
           constexpr int CPR = Cfg::RB / 16;
           ldsm4(a, (smem_u32(Ks) ^ (2 * ks % CPR * 16)) + 2 * ks / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_b16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (ks == 0) mma_b16_first(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+            else mma_b16_16816(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
   constexpr bool QK8 = Cfg::QK8;
   static_assert(CB_STAGE + 3 * STG + NFULL + RSTG <= 30, "barrier block");
   extern __shared__ unsigned char sm_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);  // (an offset: still known as shared memory)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::BAR_OFF);
   uint64_t* full = bars + CB_STAGE;     // [NFULL] the copies of a stage landed
   uint64_t* ready = full + NFULL;       // [STG] a tile may be multiplied

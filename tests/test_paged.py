@@ -215,6 +215,29 @@ def test_attention_matches_its_definition(case, e4m3):
     check_attn(c, window, run_attn(c, window))
 
 
+LOOSE = [
+    # new, past, Hq, Hkv, d, P, window, max_kv
+    ([1], [0], 4, 2, 64, 16, 0, 400000),
+    ([1, 1, 0, 1, 1], [4000, 17, 300, 31, 700], 8, 1, 64, 64, 0, 300000),
+    ([1] * 7, [5, 64, 900, 33, 1500, 0, 31], 16, 2, 128, 16, 0, 60000),
+    ([1, 2, 0, 2], [700, 95, 3, 1200], 8, 2, 32, 32, 0, 900000),
+    ([3, 1, 2], [250, 640, 1000], 12, 4, 64, 128, 90, 200000),
+    ([4, 4], [2000, 3], 16, 1, 16, 256, 0, 2000000),
+    ([1] * 130, [11 * i % 97 for i in range(130)], 2, 2, 32, 16, 0, 30000),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", LOOSE, ids=lambda c: f"{len(c[0])}x{max(c[0])}_h{c[2]}.{c[3]}_d{c[4]}_p{c[5]}_w{c[6]}")
+def test_attention_under_loose_bounds(case, e4m3):
+    """Bounds far above the lengths: the positions are shared out end to end
+    (or over many splits), most of them to nobody."""
+    new, past, Hq, Hkv, d, P, window, max_kv = case
+    c = Case(new, past, Hq, Hkv, d, P, e4m3, seed=80 + len(new) + d, pad=1)
+    c.max_kv = max_kv
+    check_attn(c, window, run_attn(c, window))
+
+
 @pytest.mark.parametrize("new", [1, 40])
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_with_large_scores_and_own_scale(e4m3, new):
