@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
     // scores: S^T[position, row]; accumulator rows gq and gq + 8 of group u
     float s[NT][NG][4];
     float kv_e[NG], inv_v[NG];
+    const uint32_t kaddr = smem_u32(Ks), vaddr = smem_u32(Vs) + voff[0];
 #pragma unroll
     for (int u = 0; u < NG; ++u) {
       if constexpr (KV8) {
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
         for (int ks = 0; ks < NKS; ++ks) {
           uint32_t a[4];
           constexpr int CPR = Cfg::RB / 16;
-          ldsm4(a, (smem_u32(Ks) ^ (2 * ks % CPR * 16)) + 2 * ks / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
+          ldsm4(a, (kaddr ^ (2 * ks % CPR * 16)) + 2 * ks / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (ks == 0) mma_b16_first(s[nt][u], a, qb[nt][ks][0], qb[nt][ks][1]);
@@ -501,9 +502,8 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
           pb[nt][1] = transpose8x8(pack_b16x2(x2, x3));
         }
       }
-      // what lies past the block's positions may hold anything: read as zeros
-      const bool tail = j0 + 16 * u + 16 > c_hi || j0 + 16 * u < t.lo;
       if constexpr (KV8) {
+        const bool tail = j0 + 16 * u + 16 > c_hi || j0 + 16 * u < t.lo;  // holds positions past the block's: as zeros
         constexpr int NB = HD / 8;  // bytes a thread reads of a V row: elements NB gq ..
         uint32_t w[4][NB >= 4 ? NB / 4 : 1];
 #pragma unroll
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
           for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][i], a, pb[nt][0], pb[nt][1]);
         }
       } else {
+        const bool tail = j0 + SW > c_hi || j0 < t.lo;
         const int jb = j0 + 16 * u + 2 * tq;
         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
         if (tail) {
@@ -553,8 +554,8 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
         for (int i = 0; i < NMT; ++i) {
           uint32_t a[4];  // matrices: positions 0-7 | 8-15 by elements 0-7 | 8-15 of step i
           constexpr int CPR = Cfg::RB / 16;
-          ldsm4_t(a, ((smem_u32(Vs) + voff[0]) ^ (2 * i % CPR * 16)) + 2 * i / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
-          a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
+          ldsm4_t(a, (vaddr ^ (2 * i % CPR * 16)) + 2 * i / CPR * SW * Cfg::RB + 16 * u * Cfg::RB);
+          if (tail) a[0] &= keep[0], a[1] &= keep[0], a[2] &= keep[1], a[3] &= keep[1];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_b16_16816(o[nt][i], a, pb[nt][0], pb[nt][1]);
         }
