@@ -20,6 +20,11 @@ silent) follow the Mamba layer the paper builds on:
 Activations between kernels are bf16 (x, z, u, the rank-R input, y, q, k, v,
 o, the outputs); B, C, delta and the states are fp32.  No norm, residual or
 MLP: these are the two token-mixing layers only.
+
+What a served stack of SWA layers has besides is at the end: the layer over a
+paged KV cache with position rotation (paged_swa_layer), for ragged batches of
+prompts, chunks and single tokens, and the norms, gates and residual sums
+between layers (paged_stack).
 """
 
 from __future__ import annotations
@@ -252,3 +257,52 @@ def swa_layer_step(hidden_t, w: SwaLayerWeights, st: SwaDecodeState, stream=None
              workspace=st.gemm_ws, stream=stream)
     o = ops.swa_step(q, k, v, st.k_ring, st.v_ring, st.pos, w.window, workspace=st.workspace, stream=stream)
     return ops.gemm(o.view(Bsz, nq), w.o_proj, workspace=st.gemm_ws, stream=stream)
+
+
+# ------------------------------------------------- ragged batches, paged cache
+def paged_swa_layer(hidden, w: SwaLayerWeights, cache, batch, freqs=None, interleaved=False, workspace=None, gemm_ws=None,
+                    stream=None):
+    """The SWA layer over a paged cache: hidden [T, d_model] bf16, the rows of
+    the ragged ``batch`` (ops.PagedBatch) -> out [T, d_model] bf16.  One
+    projection gives q, k and v; k (rotated) and v go to ``cache``
+    (ops.PagedKv), and the rotated q attend the last w.window positions there
+    (w.window 0: all).  ``freqs`` [rot / 2] fp64: the rotation's angles per
+    position (None: none).  ``workspace``: of ops.paged_attn_workspace_size
+    bytes; ``gemm_ws``: the projections' split-K workspace (up to 32 rows)."""
+    T, dm = hidden.shape
+    Hq, Hkv, d = w.heads_q, w.heads_kv, w.head_dim
+    nq, nk = Hq * d, Hkv * d
+    qkv = ops.gemm(hidden, w.qkv_proj, outs=[(torch.empty((T, nq + 2 * nk), dtype=torch.bfloat16, device=hidden.device), 0,
+                                              nq + 2 * nk, None)], workspace=gemm_ws, stream=stream)[0]
+    q, k, v = qkv[:, :nq].unflatten(1, (Hq, d)), qkv[:, nq:nq + nk].unflatten(1, (Hkv, d)), qkv[:, nq + nk:].unflatten(1, (Hkv, d))
+    q = ops.kv_append(q, k, v, cache, batch, freqs=freqs, interleaved=interleaved, stream=stream)
+    o = ops.paged_attn(q, cache, batch, window=w.window, workspace=workspace, stream=stream)
+    return ops.gemm(o.view(T, nq), w.o_proj, workspace=gemm_ws, stream=stream)
+
+
+@dataclass
+class BlockWeights:
+    """A layer of paged_stack and what stands around it."""
+    layer: SwaLayerWeights
+    w_pre: torch.Tensor                                # [d_model] fp32: the norm before the layer
+    w_post: torch.Tensor = field(default=None)         # [d_model] fp32: the norm after it
+    gate_proj: torch.Tensor = field(default=None)      # [d_model, d_model] bf16: its gate, from the layer's input
+    alpha: torch.Tensor = field(default=None)          # [d_model] fp32: its residual scale
+
+
+def paged_stack(r, blocks, w_final, caches, batch, freqs=None, interleaved=False, eps=1e-6, workspace=None, gemm_ws=None,
+                stream=None):
+    """A stack of SWA layers over paged caches: r [T, d_model] (bf16 or fp32)
+    is the residual stream, blocks a list of BlockWeights, caches one
+    ops.PagedKv a block.  Each block adds alpha * sigmoid(gate) *
+    rms(layer(n)) * w_post to r, n being the normed stream; the norm before
+    the next block comes in the same pass.  Returns (r, n): the stream and its
+    norm with w_final [d_model] fp32."""
+    _, n = ops.block_norm_fwd(r, blocks[0].w_pre, eps=eps, n_dtype=torch.bfloat16, stream=stream)
+    for i, (w, cache) in enumerate(zip(blocks, caches, strict=True)):
+        y = paged_swa_layer(n, w.layer, cache, batch, freqs=freqs, interleaved=interleaved, workspace=workspace,
+                            gemm_ws=gemm_ws, stream=stream)
+        gate = None if w.gate_proj is None else ops.gemm(n, w.gate_proj, workspace=gemm_ws, stream=stream)
+        after = blocks[i + 1].w_pre if i + 1 < len(blocks) else w_final
+        r, n = ops.block_norm_fwd(r, after, y=y, w_post=w.w_post, gate=gate, alpha=w.alpha, eps=eps, stream=stream)
+    return r, n
