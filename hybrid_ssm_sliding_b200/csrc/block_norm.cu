@@ -123,10 +123,11 @@ __device__ __forceinline__ void norm_issue(const NormInputs<NTEN>& in, const Nor
 }
 
 // Walks over this block's groups of rows: read(at) loads the thread's row into
-// registers, at(i) being tensor i's row (in the ring, whose stage is refilled
-// once all have read, or in global memory); body(row, live) computes with them.
-// Threads without a row (behind the last one) keep an earlier row's values and
-// store nothing.
+// registers, at(i) being tensor i's row (in the ring or in global memory);
+// body(row, live, release) computes with them and calls release(synced) once
+// all threads have read, that is after its first barrier (synced; release makes
+// one otherwise): the stage is then refilled.  Threads without a row (behind
+// the last one) keep an earlier row's values and store nothing.
 template <bool RING, int NTEN, class Read, class Body>
 __device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
                                           unsigned char* ring, Read&& read, Body&& body) {
@@ -136,7 +137,7 @@ __device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const Norm
     const int64_t row = g * s.rpb + sub;
     if (row < s.rows)
       read([&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + row * s.C * in.t[i].elem; });
-    body(row, row < s.rows);
+    body(row, row < s.rows, [](bool) {});
     return;
   }
   if (threadIdx.x == 0)
@@ -148,22 +149,25 @@ __device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const Norm
   int stage = 0, parity = 0;
   for (; g < s.groups; g += gridDim.x) {
     const int64_t row = g * s.rpb + sub;
-    const bool ok = mbar_wait(&sh.full[stage], parity, &sh.abort_flag);
-    const unsigned char* base = ring + stage * s.stage_bytes;
-    if (row < s.rows) read([&](int i) { return base + off[i]; });
-    if (!__syncthreads_and(ok)) {  // a wait gave up: leave once the copies in flight have landed
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[stage], parity, &sh.abort_flag))) {
+      // gave up: leave once the copies in flight have landed (threads that have
+      // left do not hold up a barrier)
       if (threadIdx.x == 0) {
         volatile int never = 0;
-        int64_t h = g + gridDim.x;
-        for (int i = 1; i < s.stages && h < s.groups; ++i, h += gridDim.x)
+        int64_t h = g;
+        for (int i = 0; i < s.stages && h < s.groups; ++i, h += gridDim.x)
           mbar_wait(&sh.full[(stage + i) % s.stages], parity ^ (stage + i >= s.stages ? 1 : 0), &never);
       }
       return;
     }
-    if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
-      norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
+    const unsigned char* base = ring + stage * s.stage_bytes;
+    if (row < s.rows) read([&](int i) { return base + off[i]; });
+    body(row, row < s.rows, [&](bool synced) {
+      if (!synced) __syncthreads();
+      if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
+        norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
+    });
     if (++stage == s.stages) stage = 0, parity ^= 1;
-    body(row, row < s.rows);
   }
 }
 
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(2)) + e[k]);
         }
       },
-      [&](int64_t row, bool live) {
+      [&](int64_t row, bool live, auto release) {
         float sum[1];
         const int64_t o = row * s.C;
         if (has_y) {
@@ -252,6 +256,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           float rs = 1.f;
           if (p.w_post) {
             row_sum(sum, sh, ph, rw);
+            release(rw.nw > 1);
             rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
             if (p.rstd_post && live && lt == 0) p.rstd_post[row] = rs;
           }
@@ -267,6 +272,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[0] = fmaf(r[i], r[i], sum[0]);
           row_sum(sum, sh, ph, rw);
+          if (!p.w_post) release(rw.nw > 1);
           const float rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
           if (p.rstd_pre && live && lt == 0) p.rstd_pre[row] = rs;
           float w[8];
@@ -276,6 +282,8 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
               store4(reinterpret_cast<YT*>(p.n) + o + e[k], w + 4 * k);
+        } else if (!p.w_post) {
+          release(false);
         }
       });
 }
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
           if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(4)) + e[k]);
         }
       },
-      [&](int64_t row, bool live) {
+      [&](int64_t row, bool live, auto release) {
         // a thread without a row must add nothing to the column sums
         const float rs = live ? rs_next : 0.f, rsy = live ? rsy_next : 0.f;
         stats(row + (int64_t)gridDim.x * s.rpb);
@@ -372,7 +380,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
             sum[2] = fmaf(ci, x[i], sum[2]);
           }
         }
-        if (has_n || p.w_post) row_sum(sum, sh, ph, rw);
+        const bool sums = has_n || p.w_post;
+        if (sums) row_sum(sum, sh, ph, rw);
+        release(sums && rw.nw > 1);
         const float m1 = rs * sum[0] * s.inv_c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = fmaf(-m1, x[i], g[i]);

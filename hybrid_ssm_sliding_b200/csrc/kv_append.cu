@@ -321,7 +321,7 @@ template <bool KV8>
 static int kv_append_go(const AppendParams& p, unsigned grid, size_t smem, cudaStream_t s) {
   static PerDeviceOnce attr;
   const int rc = once_per_device(attr, [&] {
-    return cudaFuncSetAttribute(kv_append_kernel<KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) == cudaSuccess
+    return cudaFuncSetAttribute(kv_append_kernel<KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) == cudaSuccess
                ? SAMBA_OK
                : fail(SAMBA_ERR_CUDA, "samba_kv_append: cannot set shared memory size");
   });
@@ -346,7 +346,8 @@ int launch_kv_append(const samba_kv_append_args& a, cudaStream_t s) {
   p.nq = a.q ? (page_rows + p.qrows - 1) / p.qrows * p.nhead : 0;
   const int64_t grid = (a.batch.rows / P + 2 * a.batch.batch) * ((int64_t)p.nkv + p.nq);
   if (grid > INT32_MAX) return fail(SAMBA_ERR_UNSUPPORTED, "samba_kv_append: too many rows");
-  // a block's rows are those of one page, and of one sequence
+  // a block's rows are those of one page, and of one sequence (at most 128 KB of
+  // sines; 192 KB with a slice of queries of one head)
   p.table_bytes = (p.qrows * a.rot_dim * (int)sizeof(float) + 127) / 128 * 128;
   const size_t smem = std::max<size_t>((size_t)page_rows * a.rot_dim * sizeof(float),
                                        a.q ? p.table_bytes + (size_t)p.qrows * p.qheads * head_bytes : 0);

@@ -91,6 +91,8 @@ APPEND = [
     ([17, 40], [3, 130], 6, 3, 128, 128, 64, False),
     ([33, 2], [1, 62], 3, 3, 64, 64, 0, False),
     ([1] * 40, list(range(0, 400, 10)), 4, 2, 32, 16, 32, False),
+    ([300, 5], [0, 251], 1, 1, 128, 256, 128, False),
+    ([7, 40], [12, 0], 300, 1, 128, 64, 128, False),
 ]
 
 
