@@ -27,25 +27,38 @@
 
 namespace samba {
 
-__device__ __forceinline__ void load4(float* f, const float* p) {
+// Four elements as two packed pairs: the arithmetic here is in pairs (one
+// instruction for two), which is what it takes to keep up with the memory.
+__device__ __forceinline__ void load4(f2* f, const float* p) {
   const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  f[0] = pk2(v.x, v.y), f[1] = pk2(v.z, v.w);
 }
-__device__ __forceinline__ void load4(float* f, const __nv_bfloat16* p) {
+__device__ __forceinline__ void load4(f2* f, const __nv_bfloat16* p) {
   const uint2 v = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+  f[0] = pk2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+  f[1] = pk2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
 }
-__device__ __forceinline__ void store4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void store4(float* p, const f2* f) {
+  const float2 a = up2(f[0]), b = up2(f[1]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* f) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const f2* f) {
+  const float2 u = up2(f[0]), v = up2(f[1]);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(u.x, u.y), b = __floats2bfloat162_rn(v.x, v.y);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+__device__ __forceinline__ f2 both(float x) { return pk2(x, x); }
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 t = up2(v);
+  return t.x + t.y;
+}
 
-// sigmoid(x); the fast divide gives 0 where 1 + exp(-x) passes 2^126
+// sigmoid of a pair; the fast divide gives 0 where 1 + exp(-x) passes 2^126
 __device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ f2 sigmoid2(f2 v) {
+  const float2 t = up2(v);
+  return pk2(sigmoidf(t.x), sigmoidf(t.y));
+}
 
 // How a call is cut up: rows a group, threads a row (a multiple of 32), and
 // where a tensor lies in a stage.
@@ -199,11 +212,11 @@ struct NormFwdParams {
 };
 
 // A vector's values for the thread's eight elements, 1 without one.
-__device__ __forceinline__ void load_vec(float (&f)[8], const float* w, const int (&e)[2], const bool (&has)[2]) {
+__device__ __forceinline__ void load_vec(f2 (&f)[4], const float* w, const int (&e)[2], const bool (&has)[2]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (w && has[k]) load4(f + 4 * k, w + e[k]);
-    else f[4 * k] = f[4 * k + 1] = f[4 * k + 2] = f[4 * k + 3] = 1.f;
+    if (w && has[k]) load4(f + 2 * k, w + e[k]);
+    else f[2 * k] = f[2 * k + 1] = both(1.f);
   }
 }
 
@@ -218,15 +231,15 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
   const bool has_y = p.in.t[1].p != nullptr, has_g = p.in.t[2].p != nullptr;
   const RowWarps rw(s.tpr);
   norm_setup<RING>(sh, s);
-  float wa[8], wp[8];  // w_post alpha, w_pre
+  f2 wa[4], wp[4];  // w_post alpha, w_pre
   load_vec(wa, p.w_post, e, has);
   load_vec(wp, p.alpha, e, has);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) wa[i] *= wp[i];
+  for (int i = 0; i < 4; ++i) wa[i] = mul2(wa[i], wp[i]);
   load_vec(wp, p.w_pre, e, has);
-  float r[8], y[8], z[8];  // elements that the row does not have stay zero
+  f2 r[4], y[4], z[4];  // elements that the row does not have stay zero
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = y[i] = z[i] = 0.f;
+  for (int i = 0; i < 4; ++i) r[i] = y[i] = z[i] = both(0.f);
   int ph = 0;
   norm_walk<RING>(
       p.in, s, sh, sm + kNormHead,
@@ -234,54 +247,56 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
-          load4(r + 4 * k, reinterpret_cast<const RT*>(at(0)) + e[k]);
-          if (has_y) load4(y + 4 * k, reinterpret_cast<const YT*>(at(1)) + e[k]);
-          if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(2)) + e[k]);
+          load4(r + 2 * k, reinterpret_cast<const RT*>(at(0)) + e[k]);
+          if (has_y) load4(y + 2 * k, reinterpret_cast<const YT*>(at(1)) + e[k]);
+          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(2)) + e[k]);
         }
       },
       [&](int64_t row, bool live, auto release) {
         float sum[1];
         const int64_t o = row * s.C;
         if (has_y) {
-          sum[0] = 0.f;
+          f2 q = both(0.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sum[0] = fmaf(y[i], y[i], sum[0]);
-            y[i] *= wa[i];
+          for (int i = 0; i < 4; ++i) {
+            q = fma2(y[i], y[i], q);
+            y[i] = mul2(y[i], wa[i]);
           }
           if (has_g) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= sigmoidf(z[i]);
+            for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], sigmoid2(z[i]));
           }
           float rs = 1.f;
           if (p.w_post) {
+            sum[0] = sum2(q);
             row_sum(sum, sh, ph, rw);
             release(rw.nw > 1);
             rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
             if (p.rstd_post && live && lt == 0) p.rstd_post[row] = rs;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = fmaf(y[i], rs, r[i]);
+          for (int i = 0; i < 4; ++i) r[i] = fma2(y[i], both(rs), r[i]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<RT*>(p.r_out) + o + e[k], r + 4 * k);
+              store4(reinterpret_cast<RT*>(p.r_out) + o + e[k], r + 2 * k);
         }
         if (p.n) {
-          sum[0] = 0.f;
+          f2 q = both(0.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[0] = fmaf(r[i], r[i], sum[0]);
+          for (int i = 0; i < 4; ++i) q = fma2(r[i], r[i], q);
+          sum[0] = sum2(q);
           row_sum(sum, sh, ph, rw);
           if (!p.w_post) release(rw.nw > 1);
           const float rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
           if (p.rstd_pre && live && lt == 0) p.rstd_pre[row] = rs;
-          float w[8];
+          f2 w[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = r[i] * rs * wp[i];
+          for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(r[i], both(rs)), wp[i]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<YT*>(p.n) + o + e[k], w + 4 * k);
+              store4(reinterpret_cast<YT*>(p.n) + o + e[k], w + 2 * k);
         } else if (!p.w_post) {
           release(false);
         }
@@ -314,15 +329,15 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
              has_g = p.in.t[4].p != nullptr;
   const RowWarps rw(s.tpr);
   norm_setup<RING>(sh, s);
-  float wp[8], c[8];  // w_pre, w_post alpha
+  f2 wp[4], c[4];  // w_pre, w_post alpha
   load_vec(c, p.w_post, e, has);
   load_vec(wp, p.alpha, e, has);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] *= wp[i];
+  for (int i = 0; i < 4; ++i) c[i] = mul2(c[i], wp[i]);
   load_vec(wp, p.w_pre, e, has);
-  float a_pre[8], a_post[8], dn[8], x[8], g[8], yh[8], z[8];  // elements that the row does not have stay zero
+  f2 a_pre[4], a_post[4], dn[4], x[4], g[4], yh[4], z[4];  // elements that the row does not have stay zero
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a_pre[i] = a_post[i] = dn[i] = x[i] = g[i] = yh[i] = z[i] = 0.f;
+  for (int i = 0; i < 4; ++i) a_pre[i] = a_post[i] = dn[i] = x[i] = g[i] = yh[i] = z[i] = both(0.f);
   float rs_next = 0.f, rsy_next = 1.f;
   auto stats = [&](int64_t row) {  // a row's factors, read one group ahead
     if (row >= s.rows) return;
@@ -338,12 +353,12 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
           if (has_n) {
-            load4(dn + 4 * k, reinterpret_cast<const YT*>(at(0)) + e[k]);
-            load4(x + 4 * k, reinterpret_cast<const RT*>(at(1)) + e[k]);
+            load4(dn + 2 * k, reinterpret_cast<const YT*>(at(0)) + e[k]);
+            load4(x + 2 * k, reinterpret_cast<const RT*>(at(1)) + e[k]);
           }
-          if (has_d) load4(g + 4 * k, reinterpret_cast<const RT*>(at(2)) + e[k]);
-          if (has_y) load4(yh + 4 * k, reinterpret_cast<const YT*>(at(3)) + e[k]);
-          if (has_g) load4(z + 4 * k, reinterpret_cast<const YT*>(at(4)) + e[k]);
+          if (has_d) load4(g + 2 * k, reinterpret_cast<const RT*>(at(2)) + e[k]);
+          if (has_y) load4(yh + 2 * k, reinterpret_cast<const YT*>(at(3)) + e[k]);
+          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(4)) + e[k]);
         }
       },
       [&](int64_t row, bool live, auto release) {
@@ -352,84 +367,86 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         stats(row + (int64_t)gridDim.x * s.rpb);
         if (!live) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dn[i] = x[i] = g[i] = yh[i] = 0.f;
+          for (int i = 0; i < 4; ++i) dn[i] = x[i] = g[i] = yh[i] = both(0.f);
         }
         if (!has_d) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = 0.f;
+          for (int i = 0; i < 4; ++i) g[i] = both(0.f);
         }
         const int64_t o = row * s.C;
-        float sum[3] = {0.f, 0.f, 0.f};
+        const f2 rs2 = both(rs), rsy2 = both(rsy);
+        f2 q0 = both(0.f), q1 = both(0.f), q2 = both(0.f);
         if (has_n) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] *= rs;
-            a_pre[i] = fmaf(dn[i], x[i], a_pre[i]);
-            dn[i] *= wp[i];
-            sum[0] = fmaf(dn[i], x[i], sum[0]);
-            g[i] = fmaf(rs, dn[i], g[i]);
+          for (int i = 0; i < 4; ++i) {
+            x[i] = mul2(x[i], rs2);
+            a_pre[i] = fma2(dn[i], x[i], a_pre[i]);
+            dn[i] = mul2(dn[i], wp[i]);
+            q0 = fma2(dn[i], x[i], q0);
+            g[i] = fma2(rs2, dn[i], g[i]);
           }
         }
         if (has_y) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            z[i] = has_g ? sigmoidf(z[i]) : 1.f;
-            yh[i] *= rsy;
-            const float ci = c[i] * z[i] * yh[i];
-            sum[1] = fmaf(ci, g[i], sum[1]);
-            sum[2] = fmaf(ci, x[i], sum[2]);
+          for (int i = 0; i < 4; ++i) {
+            z[i] = has_g ? sigmoid2(z[i]) : both(1.f);
+            yh[i] = mul2(yh[i], rsy2);
+            const f2 ci = mul2(mul2(c[i], z[i]), yh[i]);
+            q1 = fma2(ci, g[i], q1);
+            q2 = fma2(ci, x[i], q2);
           }
         }
+        float sum[3] = {sum2(q0), sum2(q1), sum2(q2)};
         const bool sums = has_n || p.w_post;
         if (sums) row_sum(sum, sh, ph, rw);
         release(sums && rw.nw > 1);
         const float m1 = rs * sum[0] * s.inv_c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = fmaf(-m1, x[i], g[i]);
+        for (int i = 0; i < 4; ++i) g[i] = fma2(both(-m1), x[i], g[i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-            store4(reinterpret_cast<RT*>(p.dr) + o + e[k], g + 4 * k);
+            store4(reinterpret_cast<RT*>(p.dr) + o + e[k], g + 2 * k);
         if (has_y) {
           const float m2 = p.w_post ? rsy * fmaf(-m1, sum[2], sum[1]) * s.inv_c : 0.f;
-          float dz[8], dy[8];
+          f2 dz[4], dy[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float gs = g[i] * z[i], dt = gs * c[i];
-            a_post[i] = fmaf(gs, yh[i], a_post[i]);
-            dz[i] = dt * yh[i] * (1.f - z[i]);
-            dy[i] = fmaf(rsy, dt, -yh[i] * m2);
+          for (int i = 0; i < 4; ++i) {
+            const f2 gs = mul2(g[i], z[i]), dt = mul2(gs, c[i]);
+            a_post[i] = fma2(gs, yh[i], a_post[i]);
+            dz[i] = mul2(mul2(dt, yh[i]), sub2(both(1.f), z[i]));
+            dy[i] = fma2(rsy2, dt, mul2(both(-m2), yh[i]));
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C)) {
-              store4(reinterpret_cast<YT*>(p.dy) + o + e[k], dy + 4 * k);
-              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + o + e[k], dz + 4 * k);
+              store4(reinterpret_cast<YT*>(p.dy) + o + e[k], dy + 2 * k);
+              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + o + e[k], dz + 2 * k);
             }
         }
       });
   // this block's column sums: the row slots of a group added in order, then written once
   float* mine = p.part + (int64_t)blockIdx.x * s.C;
   float* acc = reinterpret_cast<float*>(sm + kNormHead);  // [rpb][C]
-  auto put = [&](const float (&a)[8], float* dst) {
+  auto put = [&](const f2 (&a)[4], float* dst) {
     if (s.rpb == 1) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (has[k]) store4(dst + e[k], a + 4 * k);
+        if (has[k]) store4(dst + e[k], a + 2 * k);
       return;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      if (has[k]) store4(acc + sub * s.C + e[k], a + 4 * k);
+      if (has[k]) store4(acc + sub * s.C + e[k], a + 2 * k);
     __syncthreads();
     for (int i = 4 * threadIdx.x; i < s.C; i += 4 * blockDim.x) {
-      float f[4], h[4];
+      f2 f[2], h[2];
       load4(f, acc + i);
       for (int q = 1; q < s.rpb; ++q) {
         load4(h, acc + q * s.C + i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] += h[j];
+        for (int j = 0; j < 2; ++j) f[j] = add2(f[j], h[j]);
       }
       store4(dst + i, f);
     }
