@@ -10,7 +10,8 @@
 // shared memory stages: the next groups' bytes are in flight while this one
 // waits for its sums, at no cost in registers.  A call with no more groups
 // than blocks reads global memory directly, which saves the copy's latency.  A thread has two runs of four
-// elements, so that 16- and 32-bit tensors both move without a gap.
+// elements, 128 apart (a warp 256 in a row), so that 16- and 32-bit tensors both
+// move without a gap and the second run's addresses are the first's plus a constant.
 //
 // The backward pass needs one joint sum a row: with c = alpha s w_post yh and
 // s1 = sum dn w_pre x, the second norm's sum is
@@ -63,7 +64,7 @@ __device__ __forceinline__ f2 sigmoid2(f2 v) {
 // How a call is cut up: rows a group, threads a row (a multiple of 32), and
 // where a tensor lies in a stage.
 struct NormShape {
-  int64_t rows, groups;
+  uint32_t rows, groups;  // below 2^31, so that an index one step past the end still fits
   int C, rpb, tpr, stages, stage_bytes, off[5];
   float inv_c;
 };
@@ -79,32 +80,36 @@ struct NormShared {
 constexpr int kNormHead = (int)((sizeof(NormShared) + 127) / 128 * 128);
 
 // Sums of N values over the warps of a row, the same bits in every thread.
-// `ph` alternates between two slots, so one barrier per call is enough: a slot
+// The slots' two halves alternate, so one barrier per call is enough: a slot
 // is written again only after the barrier of the call in between.
 struct RowWarps {
-  int nw, w0, width;  // warps a row, the first of this row, the power of two from nw
-  __device__ RowWarps(int tpr) : nw(tpr >> 5), w0((threadIdx.x >> 5) / nw * nw), width(1) {
+  int nw, width;   // warps a row, the power of two from that
+  float* out;      // the warp's slot
+  const float* in; // the slot that the lane reads, null beyond the row's warps
+  __device__ RowWarps(NormShared& sh, int tpr) : nw(tpr >> 5), width(1) {
     while (width < nw) width *= 2;
+    const int warp = threadIdx.x >> 5, k = threadIdx.x & 31 & (width - 1);
+    out = &sh.slots[0][0][warp];
+    in = k < nw ? &sh.slots[0][0][warp / nw * nw + k] : nullptr;
   }
 };
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], NormShared& sh, int& ph, const RowWarps& rw) {
+__device__ __forceinline__ void row_sum(float (&v)[N], int& ph, const RowWarps& rw) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (rw.nw == 1) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (rw.width - 1);
-  if (lane == 0)
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) sh.slots[ph][i][warp] = v[i];
+    for (int i = 0; i < N; ++i) rw.out[ph + 32 * i] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = k < rw.nw ? sh.slots[ph][i][rw.w0 + k] : 0.f;
+  for (int i = 0; i < N; ++i) v[i] = rw.in ? rw.in[ph + 32 * i] : 0.f;
   for (int o = rw.width >> 1; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  ph ^= 1;
+  ph ^= 96;
 }
 
 // The ring over a call's input tensors.
@@ -118,21 +123,20 @@ struct NormInputs {
 };
 
 template <int NTEN>
-__device__ __forceinline__ void norm_issue(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
-                                           unsigned char* ring, int64_t group, int stage) {
-  const int64_t row0 = group * s.rpb;
-  const int n = static_cast<int>(s.rows - row0 < s.rpb ? s.rows - row0 : s.rpb) * s.C;
+__device__ __forceinline__ void norm_issue(const NormInputs<NTEN>& in, const NormShape& s, uint64_t* full,
+                                           unsigned char* stage, uint32_t group) {
+  const uint32_t row0 = group * s.rpb;
+  const uint32_t n = min(s.rows - row0, static_cast<uint32_t>(s.rpb)) * s.C;
   uint32_t bytes = 0;
 #pragma unroll
   for (int i = 0; i < NTEN; ++i)
     if (in.t[i].p) bytes += n * in.t[i].elem;
-  mbar_arrive_expect_tx(&sh.full[stage], bytes);
+  mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
   for (int i = 0; i < NTEN; ++i)
     if (in.t[i].p)
-      bulk_load(ring + stage * s.stage_bytes + s.off[i],
-                reinterpret_cast<const unsigned char*>(in.t[i].p) + row0 * s.C * in.t[i].elem, n * in.t[i].elem,
-                &sh.full[stage]);
+      bulk_load(stage + s.off[i],
+                reinterpret_cast<const unsigned char*>(in.t[i].p) + (int64_t)row0 * s.C * in.t[i].elem, n * in.t[i].elem, full);
 }
 
 // Walks over this block's groups of rows: read(at) loads the thread's row into
@@ -145,40 +149,38 @@ template <bool RING, int NTEN, class Read, class Body>
 __device__ __forceinline__ void norm_walk(const NormInputs<NTEN>& in, const NormShape& s, NormShared& sh,
                                           unsigned char* ring, Read&& read, Body&& body) {
   const int sub = threadIdx.x / s.tpr;
-  int64_t g = blockIdx.x;
+  uint32_t g = blockIdx.x, row = g * s.rpb + sub;
+  int64_t o = (int64_t)row * s.C;
   if constexpr (!RING) {  // as many blocks as groups
-    const int64_t row = g * s.rpb + sub;
     if (row < s.rows)
-      read([&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + row * s.C * in.t[i].elem; });
-    body(row, row < s.rows, [](bool) {});
+      read([&](int i) { return reinterpret_cast<const unsigned char*>(in.t[i].p) + o * in.t[i].elem; });
+    body(row, o, row < s.rows, [](bool) {});
     return;
   }
+  const uint32_t step = gridDim.x, ahead = s.stages * step;
   if (threadIdx.x == 0)
-    for (int i = 0; i < s.stages && g + (int64_t)i * gridDim.x < s.groups; ++i)
-      norm_issue(in, s, sh, ring, g + (int64_t)i * gridDim.x, i);
+    for (uint32_t i = 0; i < s.stages && g + i * step < s.groups; ++i)
+      norm_issue(in, s, &sh.full[i], ring + i * s.stage_bytes, g + i * step);
   int off[NTEN];
 #pragma unroll
   for (int i = 0; i < NTEN; ++i) off[i] = s.off[i] + sub * s.C * in.t[i].elem;
   int stage = 0, parity = 0;
-  for (; g < s.groups; g += gridDim.x) {
-    const int64_t row = g * s.rpb + sub;
+  for (; g < s.groups; g += step, row += step * s.rpb, o += (int64_t)step * s.rpb * s.C) {
     if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[stage], parity, &sh.abort_flag))) {
       // gave up: leave once the copies in flight have landed (threads that have
       // left do not hold up a barrier)
       if (threadIdx.x == 0) {
         volatile int never = 0;
-        int64_t h = g;
-        for (int i = 0; i < s.stages && h < s.groups; ++i, h += gridDim.x)
+        for (uint32_t i = 0; i < s.stages && g + i * step < s.groups; ++i)
           mbar_wait(&sh.full[(stage + i) % s.stages], parity ^ (stage + i >= s.stages ? 1 : 0), &never);
       }
       return;
     }
-    const unsigned char* base = ring + stage * s.stage_bytes;
+    unsigned char* base = ring + stage * s.stage_bytes;
     if (row < s.rows) read([&](int i) { return base + off[i]; });
-    body(row, row < s.rows, [&](bool synced) {
+    body(row, o, row < s.rows, [&](bool synced) {
       if (!synced) __syncthreads();
-      if (threadIdx.x == 0 && g + (int64_t)s.stages * gridDim.x < s.groups)
-        norm_issue(in, s, sh, ring, g + (int64_t)s.stages * gridDim.x, stage);
+      if (threadIdx.x == 0 && g + ahead < s.groups) norm_issue(in, s, &sh.full[stage], base, g + ahead);
     });
     if (++stage == s.stages) stage = 0, parity ^= 1;
   }
@@ -212,10 +214,10 @@ struct NormFwdParams {
 };
 
 // A vector's values for the thread's eight elements, 1 without one.
-__device__ __forceinline__ void load_vec(f2 (&f)[4], const float* w, const int (&e)[2], const bool (&has)[2]) {
+__device__ __forceinline__ void load_vec(f2 (&f)[4], const float* w, int e, const bool (&has)[2]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (w && has[k]) load4(f + 2 * k, w + e[k]);
+    if (w && has[k]) load4(f + 2 * k, w + e + 128 * k);
     else f[2 * k] = f[2 * k + 1] = both(1.f);
   }
 }
@@ -226,10 +228,10 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
   NormShared& sh = *reinterpret_cast<NormShared*>(sm);
   const NormShape& s = p.s;
   const int lt = threadIdx.x % s.tpr;
-  const int e[2] = {4 * lt, 4 * (lt + s.tpr)};
-  const bool has[2] = {e[0] < s.C, e[1] < s.C};
+  const int e = lt / 32 * 256 + lt % 32 * 4;
+  const bool has[2] = {e < s.C, e + 128 < s.C};
   const bool has_y = p.in.t[1].p != nullptr, has_g = p.in.t[2].p != nullptr;
-  const RowWarps rw(s.tpr);
+  const RowWarps rw(sh, s.tpr);
   norm_setup<RING>(sh, s);
   f2 wa[4], wp[4];  // w_post alpha, w_pre
   load_vec(wa, p.w_post, e, has);
@@ -247,14 +249,13 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
-          load4(r + 2 * k, reinterpret_cast<const RT*>(at(0)) + e[k]);
-          if (has_y) load4(y + 2 * k, reinterpret_cast<const YT*>(at(1)) + e[k]);
-          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(2)) + e[k]);
+          load4(r + 2 * k, reinterpret_cast<const RT*>(at(0)) + e + 128 * k);
+          if (has_y) load4(y + 2 * k, reinterpret_cast<const YT*>(at(1)) + e + 128 * k);
+          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(2)) + e + 128 * k);
         }
       },
-      [&](int64_t row, bool live, auto release) {
+      [&](uint32_t row, int64_t o, bool live, auto release) {
         float sum[1];
-        const int64_t o = row * s.C;
         if (has_y) {
           f2 q = both(0.f);
 #pragma unroll
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           float rs = 1.f;
           if (p.w_post) {
             sum[0] = sum2(q);
-            row_sum(sum, sh, ph, rw);
+            row_sum(sum, ph, rw);
             release(rw.nw > 1);
             rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
             if (p.rstd_post && live && lt == 0) p.rstd_post[row] = rs;
@@ -278,15 +279,15 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           for (int i = 0; i < 4; ++i) r[i] = fma2(y[i], both(rs), r[i]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<RT*>(p.r_out) + o + e[k], r + 2 * k);
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e + 128 * k + 4 <= s.C))
+              store4(reinterpret_cast<RT*>(p.r_out) + o + e + 128 * k, r + 2 * k);
         }
         if (p.n) {
           f2 q = both(0.f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) q = fma2(r[i], r[i], q);
           sum[0] = sum2(q);
-          row_sum(sum, sh, ph, rw);
+          row_sum(sum, ph, rw);
           if (!p.w_post) release(rw.nw > 1);
           const float rs = rsqrtf(fmaf(sum[0], s.inv_c, p.eps));
           if (p.rstd_pre && live && lt == 0) p.rstd_pre[row] = rs;
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const
           for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(r[i], both(rs)), wp[i]);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-              store4(reinterpret_cast<YT*>(p.n) + o + e[k], w + 2 * k);
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e + 128 * k + 4 <= s.C))
+              store4(reinterpret_cast<YT*>(p.n) + o + e + 128 * k, w + 2 * k);
         } else if (!p.w_post) {
           release(false);
         }
@@ -323,11 +324,11 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
   NormShared& sh = *reinterpret_cast<NormShared*>(sm);
   const NormShape& s = p.s;
   const int lt = threadIdx.x % s.tpr, sub = threadIdx.x / s.tpr;
-  const int e[2] = {4 * lt, 4 * (lt + s.tpr)};
-  const bool has[2] = {e[0] < s.C, e[1] < s.C};
+  const int e = lt / 32 * 256 + lt % 32 * 4;
+  const bool has[2] = {e < s.C, e + 128 < s.C};
   const bool has_n = p.in.t[0].p != nullptr, has_d = p.in.t[2].p != nullptr, has_y = p.in.t[3].p != nullptr,
              has_g = p.in.t[4].p != nullptr;
-  const RowWarps rw(s.tpr);
+  const RowWarps rw(sh, s.tpr);
   norm_setup<RING>(sh, s);
   f2 wp[4], c[4];  // w_pre, w_post alpha
   load_vec(c, p.w_post, e, has);
@@ -339,12 +340,12 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < 4; ++i) a_pre[i] = a_post[i] = dn[i] = x[i] = g[i] = yh[i] = z[i] = both(0.f);
   float rs_next = 0.f, rsy_next = 1.f;
-  auto stats = [&](int64_t row) {  // a row's factors, read one group ahead
+  auto stats = [&](uint32_t row) {  // a row's factors, read one group ahead
     if (row >= s.rows) return;
     if (has_n) rs_next = p.rstd_pre[row];
     if (p.w_post) rsy_next = p.rstd_post[row];
   };
-  stats((int64_t)blockIdx.x * s.rpb + sub);
+  stats(blockIdx.x * s.rpb + sub);
   int ph = 0;
   norm_walk<RING>(
       p.in, s, sh, sm + kNormHead,
@@ -353,18 +354,18 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         for (int k = 0; k < 2; ++k) {
           if (!has[k]) continue;
           if (has_n) {
-            load4(dn + 2 * k, reinterpret_cast<const YT*>(at(0)) + e[k]);
-            load4(x + 2 * k, reinterpret_cast<const RT*>(at(1)) + e[k]);
+            load4(dn + 2 * k, reinterpret_cast<const YT*>(at(0)) + e + 128 * k);
+            load4(x + 2 * k, reinterpret_cast<const RT*>(at(1)) + e + 128 * k);
           }
-          if (has_d) load4(g + 2 * k, reinterpret_cast<const RT*>(at(2)) + e[k]);
-          if (has_y) load4(yh + 2 * k, reinterpret_cast<const YT*>(at(3)) + e[k]);
-          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(4)) + e[k]);
+          if (has_d) load4(g + 2 * k, reinterpret_cast<const RT*>(at(2)) + e + 128 * k);
+          if (has_y) load4(yh + 2 * k, reinterpret_cast<const YT*>(at(3)) + e + 128 * k);
+          if (has_g) load4(z + 2 * k, reinterpret_cast<const YT*>(at(4)) + e + 128 * k);
         }
       },
-      [&](int64_t row, bool live, auto release) {
+      [&](uint32_t row, int64_t o, bool live, auto release) {
         // a thread without a row must add nothing to the column sums
         const float rs = live ? rs_next : 0.f, rsy = live ? rsy_next : 0.f;
-        stats(row + (int64_t)gridDim.x * s.rpb);
+        stats(row + gridDim.x * s.rpb);
         if (!live) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) dn[i] = x[i] = g[i] = yh[i] = both(0.f);
@@ -373,7 +374,6 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[i] = both(0.f);
         }
-        const int64_t o = row * s.C;
         const f2 rs2 = both(rs), rsy2 = both(rsy);
         f2 q0 = both(0.f), q1 = both(0.f), q2 = both(0.f);
         if (has_n) {
@@ -398,15 +398,15 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         }
         float sum[3] = {sum2(q0), sum2(q1), sum2(q2)};
         const bool sums = has_n || p.w_post;
-        if (sums) row_sum(sum, sh, ph, rw);
+        if (sums) row_sum(sum, ph, rw);
         release(sums && rw.nw > 1);
         const float m1 = rs * sum[0] * s.inv_c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = fma2(both(-m1), x[i], g[i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C))
-            store4(reinterpret_cast<RT*>(p.dr) + o + e[k], g + 2 * k);
+          if (live && has[k] && SAMBA_CHECK(row < s.rows && e + 128 * k + 4 <= s.C))
+            store4(reinterpret_cast<RT*>(p.dr) + o + e + 128 * k, g + 2 * k);
         if (has_y) {
           const float m2 = p.w_post ? rsy * fmaf(-m1, sum[2], sum[1]) * s.inv_c : 0.f;
           f2 dz[4], dy[4];
@@ -419,9 +419,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (live && has[k] && SAMBA_CHECK(row < s.rows && e[k] + 4 <= s.C)) {
-              store4(reinterpret_cast<YT*>(p.dy) + o + e[k], dy + 2 * k);
-              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + o + e[k], dz + 2 * k);
+            if (live && has[k] && SAMBA_CHECK(row < s.rows && e + 128 * k + 4 <= s.C)) {
+              store4(reinterpret_cast<YT*>(p.dy) + o + e + 128 * k, dy + 2 * k);
+              if (has_g) store4(reinterpret_cast<YT*>(p.dgate) + o + e + 128 * k, dz + 2 * k);
             }
         }
       });
@@ -432,13 +432,13 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
     if (s.rpb == 1) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (has[k]) store4(dst + e[k], a + 2 * k);
+        if (has[k]) store4(dst + e + 128 * k, a + 2 * k);
       return;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      if (has[k]) store4(acc + sub * s.C + e[k], a + 2 * k);
+      if (has[k]) store4(acc + sub * s.C + e + 128 * k, a + 2 * k);
     __syncthreads();
     for (int i = 4 * threadIdx.x; i < s.C; i += 4 * blockDim.x) {
       f2 f[2], h[2];
@@ -511,7 +511,7 @@ struct NormCut {
 };
 
 static void norm_rows(int64_t C, int& tpr, int& rpb) {
-  tpr = static_cast<int>((C / 8 + 31) / 32 * 32);
+  tpr = static_cast<int>((C + 255) / 256 * 32);
   rpb = std::max(1, 256 / tpr);
 }
 
@@ -528,10 +528,10 @@ template <int NTEN>
 static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int threads_per_sm, bool colsums) {
   NormCut c;
   NormShape& s = c.s;
-  s.rows = rows;
+  s.rows = (uint32_t)rows;
   s.C = (int)C;
   norm_rows(C, s.tpr, s.rpb);
-  s.groups = (rows + s.rpb - 1) / s.rpb;
+  s.groups = (uint32_t)((rows + s.rpb - 1) / s.rpb);
   s.inv_c = 1.f / (float)C;
   int64_t at = 0;
   for (int i = 0; i < NTEN; ++i) {
@@ -541,7 +541,7 @@ static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int
   s.stage_bytes = (int)at;
   const int per_sm = norm_blocks_per_sm(C, threads_per_sm, at);
   const int64_t most = (int64_t)sm_count() * per_sm;
-  c.grid = (int)std::min(s.groups, most);
+  c.grid = (int)std::min<int64_t>(s.groups, most);
   c.threads = s.tpr * s.rpb;
   c.ring = s.groups > most;
   s.stages = (int)std::min<int64_t>(kNormMaxStages, std::max<int64_t>(1, (kNormSmem / per_sm - kNormHead) / at));
