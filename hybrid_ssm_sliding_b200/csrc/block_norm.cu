@@ -223,7 +223,7 @@ __device__ __forceinline__ void load_vec(f2 (&f)[4], const float* w, int e, cons
 }
 
 template <typename RT, typename YT, int MAXT, bool RING>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT) block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1024 / MAXT) block_norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
   extern __shared__ __align__(128) unsigned char sm[];
   NormShared& sh = *reinterpret_cast<NormShared*>(sm);
   const NormShape& s = p.s;
@@ -498,10 +498,14 @@ __global__ void __launch_bounds__(256) block_norm_cols_kernel(const float* __res
 }
 
 // ------------------------------------------------------------------ launchers
-// Threads an SM holds (forward 1024, at 64 registers; backward 512, whose
-// column sums and gradients take more); the stages then take the shared memory.
-constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
-constexpr int kNormSmem = 200 * 1024;
+// Threads an SM holds: forward 768 at 80 registers, or 1024 at 64 where a row
+// takes more than 256 (2048 columns, bf16: 55 us where 1024 threads took 54, fp32
+// stream: 55 where they took 66); backward 512, whose column sums and gradients
+// take 120.  The stages take kFwdSmem or kBwdSmem of an SM's shared memory: enough
+// in flight, and the forward pass loses with more (32768 x 2048, fp32 stream: 130
+// KB 148 us, 200 KB 178).
+constexpr int kBwdThreadsPerSm = 512;
+constexpr int kFwdSmem = 130 * 1024, kBwdSmem = 200 * 1024;
 
 struct NormCut {
   NormShape s;
@@ -517,15 +521,15 @@ static void norm_rows(int64_t C, int& tpr, int& rpb) {
 
 // Resident blocks by threads alone; a block's stage may take a whole SM, so
 // the shared memory then allows fewer.
-static int norm_blocks_per_sm(int64_t C, int threads_per_sm, int64_t stage_bytes) {
+static int norm_blocks_per_sm(int64_t C, int threads_per_sm, int64_t stage_bytes, int smem) {
   int tpr, rpb;
   norm_rows(C, tpr, rpb);
   const int by_threads = std::max(1, threads_per_sm / (tpr * rpb));
-  return std::max<int>(1, std::min<int64_t>(by_threads, kNormSmem / (stage_bytes + kNormHead)));
+  return std::max<int>(1, std::min<int64_t>(by_threads, smem / (stage_bytes + kNormHead)));
 }
 
 template <int NTEN>
-static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int threads_per_sm, bool colsums) {
+static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int threads_per_sm, int smem, bool colsums) {
   NormCut c;
   NormShape& s = c.s;
   s.rows = (uint32_t)rows;
@@ -539,12 +543,12 @@ static NormCut norm_cut(const NormInputs<NTEN>& in, int64_t rows, int64_t C, int
     if (in.t[i].p) at += (int64_t)s.rpb * C * in.t[i].elem;
   }
   s.stage_bytes = (int)at;
-  const int per_sm = norm_blocks_per_sm(C, threads_per_sm, at);
+  const int per_sm = norm_blocks_per_sm(C, threads_per_sm, at, smem);
   const int64_t most = (int64_t)sm_count() * per_sm;
   c.grid = (int)std::min<int64_t>(s.groups, most);
   c.threads = s.tpr * s.rpb;
   c.ring = s.groups > most;
-  s.stages = (int)std::min<int64_t>(kNormMaxStages, std::max<int64_t>(1, (kNormSmem / per_sm - kNormHead) / at));
+  s.stages = (int)std::min<int64_t>(kNormMaxStages, std::max<int64_t>(1, (smem / per_sm - kNormHead) / at));
   c.smem = kNormHead + (c.ring ? (size_t)s.stages * s.stage_bytes : 0);
   if (colsums && s.rpb > 1) c.smem = std::max(c.smem, kNormHead + (size_t)s.rpb * C * sizeof(float));
   return c;
@@ -567,6 +571,9 @@ static int norm_go(const NormCut& c, const P& p, cudaStream_t s, const char* who
 template <typename RT, typename YT>
 static int norm_fwd_t(const NormCut& c, const NormFwdParams& p, cudaStream_t s) {
   const char* who = "samba_block_norm_fwd";
+  if (c.threads <= 256)
+    return c.ring ? norm_go<block_norm_fwd_kernel<RT, YT, 256, true>>(c, p, s, who)
+                  : norm_go<block_norm_fwd_kernel<RT, YT, 256, false>>(c, p, s, who);
   if (c.threads <= 512)
     return c.ring ? norm_go<block_norm_fwd_kernel<RT, YT, 512, true>>(c, p, s, who)
                   : norm_go<block_norm_fwd_kernel<RT, YT, 512, false>>(c, p, s, who);
@@ -590,7 +597,7 @@ int launch_block_norm_fwd(const samba_block_norm_args& a, cudaStream_t s) {
   const int re = rb ? 2 : 4, ye = yb ? 2 : 4;
   NormFwdParams p = {{{{a.r, re}, {a.y, ye}, {a.gate, ye}}}, a.w_pre, a.w_post, a.alpha, a.r_out, a.n, a.rstd_pre,
                      a.rstd_post, {}, a.eps};
-  const NormCut c = norm_cut(p.in, a.rows, a.width, kFwdThreadsPerSm, false);
+  const NormCut c = norm_cut(p.in, a.rows, a.width, a.width <= 2048 ? 768 : 1024, kFwdSmem, false);
   p.s = c.s;
   if (rb && yb) return norm_fwd_t<__nv_bfloat16, __nv_bfloat16>(c, p, s);
   if (rb) return norm_fwd_t<__nv_bfloat16, float>(c, p, s);
@@ -601,7 +608,7 @@ int launch_block_norm_fwd(const samba_block_norm_args& a, cudaStream_t s) {
 size_t block_norm_bwd_workspace(int64_t rows, int64_t C) {
   int tpr, rpb;
   norm_rows(C, tpr, rpb);
-  const int64_t most = (int64_t)sm_count() * norm_blocks_per_sm(C, kBwdThreadsPerSm, 0);
+  const int64_t most = (int64_t)sm_count() * norm_blocks_per_sm(C, kBwdThreadsPerSm, 0, kBwdSmem);
   return (size_t)std::min<int64_t>((rows + rpb - 1) / rpb, most) * 2 * (size_t)C * sizeof(float);
 }
 
@@ -619,7 +626,7 @@ int launch_block_norm_bwd(const samba_block_norm_bwd_args& a, cudaStream_t s) {
   NormBwdParams p = {{{{a.dn, ye}, {a.dn ? a.r : nullptr, re}, {a.dr_out, re}, {a.y, ye}, {a.gate, ye}}},
                      a.w_pre, a.rstd_pre, a.w_post, a.rstd_post, a.alpha, a.dr, a.dy, a.dgate,
                      reinterpret_cast<float*>(a.workspace), {}};
-  const NormCut c = norm_cut(p.in, a.rows, a.width, kBwdThreadsPerSm, true);
+  const NormCut c = norm_cut(p.in, a.rows, a.width, kBwdThreadsPerSm, kBwdSmem, true);
   p.s = c.s;
   int rc;
   if (rb && yb) rc = norm_bwd_t<__nv_bfloat16, __nv_bfloat16>(c, p, s);
