@@ -136,5 +136,5 @@ def test_norm_backward_refuses(lib, over, code):
 def test_norm_backward_workspace_size(lib):
     size = lib.samba_block_norm_bwd_workspace_size
     assert size(0, 256) == 0 and size(4, 0) == 0
-    # three planes of column sums for each group of rows (one of 2048 elements, eight of 256)
-    assert size(1, 2048) == 3 * 2048 * 4 and size(8, 256) == 3 * 256 * 4
+    # two planes of column sums for each group of rows (one of 2048 elements, eight of 256)
+    assert size(1, 2048) == 2 * 2048 * 4 and size(8, 256) == 2 * 256 * 4
