@@ -10,15 +10,15 @@
 //
 // Bytes bound the call (q in and out, k and v in, the cache rows out).  Its
 // items are the (sequence, page) pairs, which is what a scale belongs to.  An
-// item has blocks for eight of its (matrix, kv head) blocks each, a warp one,
-// and blocks for a slice of its rows' queries each; a block brings the sines
-// and cosines of its rows to shared memory once for all its heads.  Items of a
-// sequence are numbered from floor(q_start / page) + 2 b, which needs no prefix
-// sum and leaves each sequence at least as many numbers as it touches pages.
-// A block of queries asks for its whole slice at once (a bulk copy a row, into
-// shared memory) before it works out the sines: the latency of loads, not the
-// arithmetic, is what kept a version with loads to registers at 93 us where
-// this one takes 77 (41k rows of 32 + 8 heads of 64).
+// item has blocks for some of its (matrix, kv head) pairs each, and blocks for a
+// slice of its rows' queries each; a block brings the sines and cosines of its
+// rows to shared memory once for all its heads.  Items of a sequence are
+// numbered from floor(q_start / page) + 2 b, which needs no prefix sum and leaves
+// each sequence at least as many numbers as it touches pages.
+// A block asks for all of its rows at once (bulk copies into shared memory)
+// before it works out the sines: the latency of loads, not the arithmetic, is
+// what kept a version with loads to registers at 93 us where this one takes 74
+// (41k rows of 32 + 2 x 4 heads of 64, 8 bits).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -29,12 +29,14 @@ namespace samba {
 
 struct AppendParams {
   samba_kv_append_args a;
-  // blocks an item for keys and values, for queries; slices of the query heads,
-  // heads and rows of one; bytes of the sines before a slice's queries
-  int nkv, nq, nhead, qheads, qrows, table_bytes;
+  // blocks an item for keys and values, for queries; (matrix, kv head) units of
+  // one of the former; slices of the query heads, heads and rows of one; bytes of
+  // the sines before a block's rows
+  int nkv, nq, kvu, nhead, qheads, qrows, kv_table_bytes, table_bytes;
 };
 
 constexpr int kAppendThreads = 256, kAppendBlocks = 3;  // three blocks an SM: 80 registers
+constexpr int kKvBytes = 32 * 1024;                     // rows of keys and values a block
 constexpr int kSliceBytes = 64 * 1024;                  // a slice of queries (48 KB, four blocks of 64 registers: 97 us)
 
 __device__ __forceinline__ void bf16x8_to_f32(uint4 v, float (&f)[8]) {
@@ -113,26 +115,12 @@ __device__ __forceinline__ float finite_abs(float x) {  // |x|, 0 for NaN and in
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
-// body(r, pair) for the rows r = first, first + step .. below n, the loads of
-// two rows under way together.
-template <class Load, class Body>
-__device__ __forceinline__ void for_rows(int first, int step, int n, Load&& load, Body&& body) {
-  for (int r = first; r < n; r += 2 * step) {
-    RawPair raw[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (r + k * step < n) raw[k] = load(r + k * step);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (r + k * step < n) body(r + k * step, raw[k]);
-  }
-}
-
 template <bool KV8>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(128) float table[];  // [rows][rot / 2] cosines, then sines; a slice's queries
   __shared__ int span[3];                          // q_start[b], q_start[b + 1], kv_len[b]
   __shared__ uint64_t landed;                      // the slice's copies
+  __shared__ float warp_max[kAppendThreads / 32];
   __shared__ int abort_flag;
   const samba_kv_append_args& a = p.a;
   const int P = a.kv.page_size, d = a.kv.head_dim, Hkv = a.kv.heads_kv, Hq = a.heads_q, rot = a.rot_dim;
@@ -226,50 +214,78 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
     }
     return;
   }
-  // keys and values: one warp a (matrix, kv head), keys first
+  // Keys and values: the block's units are (matrix, kv head) pairs, keys first,
+  // 8 / kvu warps each; their rows are copied to shared memory like the queries.
   const int page = a.batch.block_table[(int64_t)b * a.batch.max_pages + col];
   if (page < 0 || page >= a.kv.num_pages) {
     if (tid == 0 && part == 0) report_batch();
     return;
   }
-  const int off = lo - (col << pshift), u = part * (kAppendThreads / 32) + warp;
-  if (part * (kAppendThreads / 32) < Hkv) fill();
-  if (u >= 2 * Hkv) return;
-  const bool is_v = u >= Hkv;
+  const int off = lo - (col << pshift);
+  const int u0 = part * p.kvu, u1 = min(u0 + p.kvu, 2 * Hkv);
+  const int kc = max(0, min(u1, Hkv) - u0), v0 = max(u0 - Hkv, 0), vc = u1 - u0 - kc, row_elems = (kc + vc) * d;
+  __nv_bfloat16* in = reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<unsigned char*>(table) + p.kv_table_bytes);
+  if (warp == 0) {
+    if (lane == 0) mbar_arrive_expect_tx(&landed, n * row_elems * 2);
+    __syncwarp();
+    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k) + (int64_t)row0 * a.ldk + (int64_t)u0 * d;
+    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v) + (int64_t)row0 * a.ldv + (int64_t)v0 * d;
+    for (int r = lane; r < n; r += 32) {
+      if (kc > 0) bulk_load(in + r * row_elems, k + r * a.ldk, kc * d * 2, &landed);
+      if (vc > 0) bulk_load(in + r * row_elems + kc * d, v + r * a.ldv, vc * d * 2, &landed);
+    }
+  }
+  const int wpu = kAppendThreads / 32 / p.kvu, sw = warp & (wpu - 1), ul = warp / wpu, u = u0 + ul;
+  const bool unit = u < u1, is_v = u >= Hkv;
   const int h = is_v ? u - Hkv : u;
-  const int64_t ld = is_v ? a.ldv : a.ldk;
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + (int64_t)row0 * ld + (int64_t)h * d;
-  const int64_t blk = ((int64_t)page * Hkv + h) * P;  // row of the (page, head) block
-  // a lane takes the same chunk of every 32 / PC-th row
-  const int c = lane & (PC - 1), r0 = lane >> pcshift, rstep = 32 >> pcshift;
+  const int64_t block = (int64_t)page * Hkv + (unit ? h : 0);  // the (page, head) block
+  float* scale = nullptr;
+  float was_scale = 0.f;
+  if constexpr (KV8) {
+    scale = (is_v ? a.kv.v_scale : a.kv.k_scale) + block;
+    if (unit && off > 0) was_scale = *scale;
+  }
+  if (kc > 0) fill();
+  if (!__syncthreads_and(mbar_wait(&landed, 0, &abort_flag))) {
+    volatile int never = 0;
+    if (tid == 0) mbar_wait(&landed, 0, &never);  // (copies still in flight)
+    return;
+  }
+  // a lane takes the same chunk of every rstep-th row
+  const int c = lane & (PC - 1), r0 = (lane >> pcshift) + sw * (32 >> pcshift), rstep = wpu * (32 >> pcshift);
   const PairChunk pc = pair_chunk(c, is_v ? 0 : rot, inter);
-  auto load = [&](int r) { return load_pair(src + r * ld, pc); };
-  auto turned = [&](int r, const RawPair& raw, float (&x)[8], float (&y)[8]) {
+  const __nv_bfloat16* src = in + ul * d;
+  auto turned = [&](int r, float (&x)[8], float (&y)[8]) {
     Turn t;
     if (pc.rot) load_turn(t, co + r * half + 8 * c, si + r * half + 8 * c);
-    rotate(raw, pc.rot, inter, t, x, y);
+    rotate(load_pair(src + r * row_elems, pc), pc.rot, inter, t, x, y);
   };
   if constexpr (KV8) {
-    uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + blk * d;
-    float* scale = (is_v ? a.kv.v_scale : a.kv.k_scale) + (int64_t)page * Hkv + h;
-    const float was_scale = off > 0 ? *scale : 0.f;
     float amax = 0.f;  // of finite values; infinities are looked at again only where there are any
     for (int finite = 0; finite < 2; ++finite) {
       amax = 0.f;
-      for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
-        float x[8], y[8];
-        turned(r, raw, x, y);
-        if (finite) {
+      if (unit)
+#pragma unroll 2
+        for (int r = r0; r < n; r += rstep) {
+          float x[8], y[8];
+          turned(r, x, y);
+          if (finite) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = finite_abs(x[e]), y[e] = finite_abs(y[e]);
+            for (int e = 0; e < 8; ++e) x[e] = finite_abs(x[e]), y[e] = finite_abs(y[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));  // (NaN is passed over)
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));  // (NaN is passed over)
-      });
-#pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (amax <= 3.402823466e38f) break;
+      if (lane == 0) warp_max[warp] = amax;
+      const bool all_finite = !__syncthreads_or(amax > 3.402823466e38f);
+      for (int w = 0; w < wpu; ++w) amax = fmaxf(amax, warp_max[ul * wpu + w]);
+      if (all_finite) break;
+      __syncthreads();
     }
+    if (!unit) return;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + block * P * d;
     int k = scale_exponent(amax);
     if (off > 0) {  // the page holds earlier rows at its old scale
       const int was = stored_exponent(was_scale);
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
       if (k > was) {  // code * 2^(was - k), re-rounded
         const float by = exp2i(was - k);
         uint4* old = reinterpret_cast<uint4*>(dst);
-        for (int i = lane; i < off * d / 16; i += 32) {
+        for (int i = sw * 32 + lane; i < off * d / 16; i += 32 * wpu) {
           uint4 v = old[i];
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -291,29 +307,32 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
         }
       }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0 && SAMBA_CHECK(page < a.kv.num_pages && h < Hkv)) *scale = exp2i(k);
+    // (every warp of the unit read the old scale before the barriers above)
+    if (lane == 0 && sw == 0 && SAMBA_CHECK(page < a.kv.num_pages && h < Hkv)) *scale = exp2i(k);
     const float inv = exp2i(-k);
-    for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
+#pragma unroll 2
+    for (int r = r0; r < n; r += rstep) {
       float x[8], y[8];
-      turned(r, raw, x, y);
+      turned(r, x, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= inv, y[e] *= inv;
       uint8_t* to = dst + (off + r) * d;
-      if (!SAMBA_CHECK(off + r < P)) return;
+      if (!SAMBA_CHECK(off + r < P)) continue;
       *reinterpret_cast<uint2*>(to + pc.lo) = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
       *reinterpret_cast<uint2*>(to + pc.hi) = make_uint2(to_e4m3x4(y[0], y[1], y[2], y[3]), to_e4m3x4(y[4], y[5], y[6], y[7]));
-    });
+    }
   } else {
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.kv.v : a.kv.k) + blk * d;
-    for_rows(r0, rstep, n, load, [&](int r, const RawPair& raw) {
+    if (!unit) return;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.kv.v : a.kv.k) + block * P * d;
+#pragma unroll 2
+    for (int r = r0; r < n; r += rstep) {
       float x[8], y[8];
-      turned(r, raw, x, y);
+      turned(r, x, y);
       __nv_bfloat16* to = dst + (off + r) * d;
-      if (!SAMBA_CHECK(off + r < P)) return;
+      if (!SAMBA_CHECK(off + r < P)) continue;
       *reinterpret_cast<uint4*>(to + pc.lo) = f32_to_bf16x8(x);
       *reinterpret_cast<uint4*>(to + pc.hi) = f32_to_bf16x8(y);
-    });
+    }
   }
 }
 
@@ -337,7 +356,11 @@ int launch_kv_append(const samba_kv_append_args& a, cudaStream_t s) {
   AppendParams p;
   p.a = a;
   const int page_rows = (int)std::min<int64_t>(P, a.batch.max_q), head_bytes = a.kv.head_dim * 2;
-  p.nkv = (2 * a.kv.heads_kv + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  // units of keys and values: as many as kKvBytes hold, one of 256 rows of 128 always
+  p.kvu = kAppendThreads / 32;
+  while (p.kvu > 1 && (p.kvu * page_rows * head_bytes > kKvBytes || p.kvu >= 4 * a.kv.heads_kv)) p.kvu /= 2;
+  p.nkv = (2 * a.kv.heads_kv + p.kvu - 1) / p.kvu;
+  p.kv_table_bytes = (page_rows * a.rot_dim * (int)sizeof(float) + 127) / 128 * 128;
   // a slice: whole rows, or for very wide ones a row's share of the heads
   p.qheads = std::min(std::max(1, a.heads_q), kSliceBytes / head_bytes);
   p.nhead = a.q ? (a.heads_q + p.qheads - 1) / p.qheads : 1;
@@ -349,7 +372,7 @@ int launch_kv_append(const samba_kv_append_args& a, cudaStream_t s) {
   // a block's rows are those of one page, and of one sequence (at most 128 KB of
   // sines; 192 KB with a slice of queries of one head)
   p.table_bytes = (p.qrows * a.rot_dim * (int)sizeof(float) + 127) / 128 * 128;
-  const size_t smem = std::max<size_t>((size_t)page_rows * a.rot_dim * sizeof(float),
+  const size_t smem = std::max<size_t>(p.kv_table_bytes + (size_t)p.kvu * page_rows * head_bytes,
                                        a.q ? p.table_bytes + (size_t)p.qrows * p.qheads * head_bytes : 0);
   return a.kv.dtype == SAMBA_E4M3 ? kv_append_go<true>(p, (unsigned)grid, smem, s)
                                   : kv_append_go<false>(p, (unsigned)grid, smem, s);
