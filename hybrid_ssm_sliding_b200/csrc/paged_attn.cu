@@ -741,14 +741,15 @@ static PagedPlan paged_plan(const samba_paged_attn_args& a) {
   const int64_t rows = std::max<int64_t>(1, a.batch.max_q) * group;
   pl.chunk_kernel = rows > kFewRows;
   if (pl.chunk_kernel) {
-    // one block an SM: key tiles are split while units leave SMs idle, at least four tiles each
+    // one block of 256 rows an SM or two of 128: key tiles are split while units leave SMs idle, at least four tiles each
+    const int64_t unit = paged_unit(a);
     pl.nt = pl.chunk = 0;
     pl.cluster = 1;
-    pl.ntile = (int)((rows + 255) / 256);
+    pl.ntile = (int)((rows + unit - 1) / unit);
     int64_t span = a.batch.max_kv;
-    if (a.window > 0) span = std::min<int64_t>(span, a.window + 256 / group + 128);
+    if (a.window > 0) span = std::min<int64_t>(span, a.window + unit / group + 128);
     const int64_t units = (int64_t)pl.ntile * a.kv.heads_kv * std::max<int64_t>(1, a.batch.batch);
-    pl.nsplit = pl.npart = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sm_count() / units, span / 512));
+    pl.nsplit = pl.npart = (int)std::max<int64_t>(1, std::min<int64_t>(256 / unit * sm_count() / units, span / 512));
     return pl;
   }
   pl.nt = rows <= 8 ? 1 : 2;

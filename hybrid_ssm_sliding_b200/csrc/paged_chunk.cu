@@ -2,29 +2,41 @@
 // cores (paged_attn.cu takes calls of a few rows a sequence).
 //
 // o = softmax(scale Q K^T + mask) V with the softmax's running maximum and sum
-// over key tiles of 128 positions.  A work unit is 256 rows of one sequence
-// and kv head, row = token * group + head, as two tiles of 128 rows that are
-// processed in turn, so that every K/V tile serves 256 rows.  The exponentials
-// (128 x 256 a key tile) bound it, then the products: 4 HD flops each.
+// over key tiles of 128 positions.  A work unit is one or two tiles of 128 rows of
+// a sequence and kv head, row = token * group + head.  The exponentials (128 x 128
+// a key tile and row tile) would bound it, then the products (4 HD flops each); what
+// it does not reach of that goes to the chain of a row tile: scores, softmax and
+// products, one after the other.  Two chains an SM fill each other's gaps:
 //
-// Warps 0-3 and 4-7 are the softmax of the two row tiles, a thread a row: they
-// bring their rows of Q to shared memory, read S from tensor memory, write P
-// back and rescale O when the maximum grows by more than 2^8.  Warp 8 copies
-// pages (a lane a page), warps 9 and 10 issue the two tiles' products.  Warp 11
-// (bf16 cache) or warps 12-15 (8 bits) make a copied tile fit to be
-// multiplied: positions that no row sees become zeros in V, whose content may
-// be anything, and e4m3 codes become f16 (exact).
+// 8 bits, up to a head dimension of 64: a block has one row tile and half of an
+// SM's tensor and shared memory, so two blocks share an SM.  One's start and end
+// fall under the other's exponentials, and the last round of units leaves less idle
+// (4 sequences of 1536 rows, 32 heads, windows of 2048: 118 us, two tiles a block
+// 130; 8192 rows: 474 and 519).
 //
-// 8 bits: with value = code * scale a position's key scale multiplies its
-// scores and the value scale's exponent joins the exponent of its probability,
-// p' = 2^(s + e - m), m the running maximum of s + e; the sum takes p' 2^-e.
-// Both are constant over a page, so they cost one multiply a group of 16
-// positions, or of 64 where pages are as long (a compiled size, SPAN: 48.2 and
-// 47.0 us for 1184 tokens of 32 heads over a window of 2048).  (A head dimension of 16 is below the 32
-// elements of an 8-bit product: K and Q become f16 there.)
+// bf16, or a head dimension of 128, whose tiles do not fit twice: a block has two
+// row tiles that share its keys (bf16, head dimension 64, 4736 rows of 32 heads:
+// 136 us, 147 with a tile a block, which copies the keys twice as often).  With
+// 128 P takes the place of S, and S of the next key tile waits for P V.
 //
-// A head dimension of 128 leaves no room in tensor memory for P beside S and
-// O: P then takes the place of S, and S of the next tile waits for P V.
+// Four warps a row tile are its softmax, a thread a row: they bring their rows of
+// Q to shared memory, read S from tensor memory, write P back and rescale O when
+// the maximum grows by more than 2^8.  One warp copies pages (a lane a page), one a
+// row tile issues the products.  One more (bf16 cache), two or four (8 bits) make a
+// copied tile of V fit to be multiplied: positions that no row sees, whose content
+// may be anything, become zeros, and e4m3 codes become f16 (exact).
+//
+// 8 bits: K's codes are multiplied as they are.  A row of Q, brought to a
+// maximum of 2^7 to 2^8 by a power of two, is the sum of two e4m3 numbers, the
+// nearest one and what that leaves: four significant bits each give bf16's
+// eight, down to 2^-10 of the row's maximum (below, the error is 2^-18 of it).
+// With value = code * scale a position's key scale multiplies its scores and the
+// value scale's exponent joins the exponent of its probability, p' = 2^(s + e -
+// m), m the running maximum of s + e; the sum takes p' 2^-e.  Both are constant
+// over a page, so they cost one multiply a group of 16 positions, or of 64 where
+// pages are as long (a compiled size, SPAN).  An 8-bit product takes 32 elements:
+// with a head dimension of 16 the other half of Q and K is zeros, K's filled in by
+// the copies, whose box is wider than the pool's rows.
 #include <algorithm>
 #include <cmath>
 
@@ -37,32 +49,45 @@ namespace samba {
 
 template <int HD, bool KV8>
 struct ChunkCfg {
-  static constexpr bool QK8 = KV8 && HD >= 32;              // 8-bit products for S
+  static constexpr int NX = KV8 && HD <= 64 ? 1 : 2;        // row tiles a block (paged_unit has the same rule)
   static constexpr int RB = HD * 2 < 128 ? HD * 2 : 128;    // bytes of a panel's row = swizzle span
   static constexpr int NP = HD * 2 / RB;                    // panels a matrix
   static constexpr int PANEL = 128 * RB;
   static constexpr int TILE = NP * PANEL;                   // 128 rows of 16-bit elements
   static constexpr int RAW = 128 * HD;                      // 128 rows of codes
-  static constexpr int QRB = QK8 ? HD : RB;                 // the same for Q and K (Q: two matrices of codes)
-  static constexpr int KTILE = QK8 ? RAW : TILE;
-  static constexpr int STG = HD == 128 ? 2 : 4;             // K/V tiles ready for the products
-  static constexpr int RSTG = KV8 ? 2 : 0;                  // copied tiles of codes (QK8: of V)
-  static constexpr int RAWS = QK8 ? RAW : 2 * RAW;          // bytes of one
-  static constexpr int NFULL = KV8 ? RSTG : STG;
+  static constexpr int KD = KV8 && HD < 32 ? 32 : HD;       // elements of a row of Q and K
+  static constexpr int QRB = KV8 ? KD : RB;                 // the span of Q and K (Q: two matrices of codes)
+  static constexpr int KTILE = KV8 ? 128 * KD : TILE, QTILE = KV8 ? 2 * KTILE : TILE;
+  static constexpr int VS = HD == 128 || KV8 ? 2 : 4;       // tiles of V ready for the products
+  static constexpr int RSTG = KV8 ? 2 : 0;                  // copied tiles of V's codes
+  // Tiles of K: as many as the copies' waits for V free as well.  (Two row tiles:
+  // these wait until V of tile it - VS was multiplied, though codes of it were
+  // copied away before: 128, 8 bits, 1184 rows of 32 heads 60 us, 66 without,
+  // as the row tiles then reach their exponentials together.)
+  static constexpr int KS = NX == 2 ? VS : VS + RSTG;
+  static constexpr int NFULL = KV8 ? RSTG : VS;
   static constexpr bool AHEAD = HD <= 64;                   // S of the next tile beside P
-  static constexpr int Q_OFF = 0, K_OFF = 2 * TILE, V_OFF = K_OFF + STG * KTILE, RAW_OFF = V_OFF + STG * TILE;
-  static constexpr int BAR_OFF = RAW_OFF + RSTG * RAWS;
-  static constexpr int SC_OFF = BAR_OFF + 256;              // [RSTG + STG][8] scale pairs
-  static constexpr int SMEM = SC_OFF + (RSTG + STG) * 64 + 1024;
+  static constexpr int Q_OFF = 0, K_OFF = NX * QTILE, V_OFF = K_OFF + KS * KTILE, RAW_OFF = V_OFF + VS * TILE;
+  static constexpr int BAR_OFF = RAW_OFF + RSTG * RAW;
+  static constexpr int SC_OFF = BAR_OFF + 512;              // [8 tiles][8] scale pairs
+  static constexpr int SMEM = SC_OFF + (KV8 ? 512 : 0) + 1024;
   static constexpr int swz(int rb) { return rb == 128 ? 2 : rb == 64 ? 4 : 6; }  // descriptors' swizzle codes
-  // Of each eight pairs of probabilities, so many go to the FMA pipe (bf16, 64:
-  // none, 1, 2 of them 459, 439, 414 us for 8192 rows of 32 heads)
-  static constexpr int POLY = KV8 || HD == 128 ? 1 : 2;
-  static constexpr int THREADS = KV8 ? 512 : 384;
-  static constexpr int CONV_WARP0 = KV8 ? 12 : 11, CONV_WARPS = KV8 ? 4 : 1;
-  static constexpr uint32_t COL_S = 0, COL_P = AHEAD ? 256 : 0, COL_O = AHEAD ? 384 : 256;
-  static constexpr uint32_t P_STEP = AHEAD ? 64 : 128, O_STEP = AHEAD ? 64 : 128;  // tile B's columns after A's
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // Of each eight pairs of probabilities, so many go to the FMA pipe (bf16, 64,
+  // 4736 rows: 1 of them 141 us, 2 139; a tile a block: 1 121 us, none 118)
+  static constexpr int POLY = NX == 1 ? 0 : HD == 128 ? 1 : 2;
+  // warps: softmax, copies, products (one a row tile), V
+  static constexpr int W_COPY = 4 * NX, W_MMA = W_COPY + 1, CONV_WARPS = !KV8 ? 1 : NX == 1 ? 2 : 4;
+  static constexpr int WARPS = W_COPY + (KV8 && NX == 2 ? 8 : 4), W_CONV = WARPS - CONV_WARPS;
+  static constexpr int THREADS = 32 * WARPS, BLOCKS = NX == 1 ? 2 : 1;
+  // Registers a thread at launch, of the softmax warps and of the others: the
+  // shares add up to the launch's.
+  static constexpr int R0 = KV8 ? 128 : 168;
+  static constexpr int R_SOFT = !KV8 ? 208 : NX == 2 ? 192 : 200, R_REST = !KV8 ? 88 : NX == 2 ? 64 : 56;
+  static_assert(128 * NX * R_SOFT + (THREADS - 128 * NX) * R_REST == THREADS * R0, "registers");
+  static constexpr uint32_t TMEM = NX == 2 ? 512 : 256;
+  static constexpr uint32_t COL_S = 0, COL_P = !AHEAD ? 0 : 128 * NX, COL_O = !AHEAD ? 256 : 192 * NX,
+                            STEP = AHEAD ? 64 : 128;  // (P's and O's columns of a tile after another's)
+  static_assert(SMEM <= (NX == 1 ? 113 : 227) * 1024, "shared memory");
 };
 
 // Barriers, each per row tile x: Q written, S ready, S read, P ready, O done,
@@ -77,7 +102,7 @@ struct ChunkParams {
   const float* v_scale;
   samba_paged_batch batch;
   int64_t num_pages, window;
-  int Hq, Hkv, group, page_shift, units, nsplit;  // units: pairs of row tiles a sequence may have
+  int Hq, Hkv, group, page_shift, units, nsplit;  // units a sequence may have
   float scale_log2;
 };
 
@@ -140,25 +165,25 @@ __device__ __forceinline__ float2 chunk_ex2_poly(float2 v) {
 }
 
 template <int HD, bool KV8, int SPAN>
-__global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
+__global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>::BLOCKS)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const ChunkParams p) {
   using Cfg = ChunkCfg<HD, KV8>;
-  constexpr int STG = Cfg::STG, RSTG = Cfg::RSTG, NFULL = Cfg::NFULL;
-  constexpr bool QK8 = Cfg::QK8;
-  static_assert(CB_STAGE + 3 * STG + NFULL + RSTG <= 30, "barrier block");
+  constexpr int NX = Cfg::NX, KS = Cfg::KS, VS = Cfg::VS, RSTG = Cfg::RSTG, NFULL = Cfg::NFULL;
+  static_assert(NX == 2 || KV8, "the copies' waits");
+  static_assert(CB_STAGE + KS + NFULL + 2 * VS + RSTG + 8 <= 62, "barrier block");
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);  // (an offset: still known as shared memory)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::BAR_OFF);
-  uint64_t* full = bars + CB_STAGE;     // [NFULL] the copies of a stage landed
-  uint64_t* ready = full + NFULL;       // [STG] a tile may be multiplied
-  uint64_t* empty = ready + STG;        // [STG] both row tiles are done with it
-  uint64_t* rawempty = empty + STG;     // [RSTG] the codes were converted
-  uint64_t* kfull = rawempty + RSTG;    // [STG] QK8: the tile of K landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
+  uint64_t* kfull = bars + CB_STAGE;    // [KS] a tile of K landed
+  uint64_t* full = kfull + KS;          // [NFULL] a tile of V landed
+  uint64_t* ready = full + NFULL;       // [VS] it may be multiplied
+  uint64_t* vempty = ready + VS;        // [VS] its products are done
+  uint64_t* rawempty = vempty + VS;     // [RSTG] its codes were converted
+  uint64_t* scales = rawempty + RSTG;   // [8] 8 bits: the scales of a tile (slot t mod 8) are there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 62);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float2* sc_raw = reinterpret_cast<float2*>(sm + Cfg::SC_OFF);  // [RSTG][8] key scale, value scale exponent
-  float2* sc_tile = sc_raw + RSTG * 8;                           // [STG][8]
+  float2* sc_tile = reinterpret_cast<float2*>(sm + Cfg::SC_OFF);  // [8][8] key scale, value scale exponent
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = 1 << p.page_shift;
 
@@ -169,7 +194,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
   const int b = rest % static_cast<int>(p.batch.batch), g = blockIdx.y;
   const int unit = p.units - 1 - rest / static_cast<int>(p.batch.batch);
   const SeqSpan sq = seq_span(p.batch, P, b, unit == 0 && split == 0 && g == 0 && threadIdx.x == 0);
-  const int row0 = unit * 256, nrow = min(256, sq.n * p.group - row0);
+  const int row0 = unit * (128 * NX), nrow = min(128 * NX, sq.n * p.group - row0);
   if (nrow <= 0) return;
   const int first = sq.kv - sq.n;  // position of the sequence's first row
   const int hi = first + (row0 + nrow - 1) / p.group + 1;
@@ -194,7 +219,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
 
   const bool two = nrow > 128;  // the second row tile has rows
   if (threadIdx.x == 0) {
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NX; ++x) {
       mbar_init(&bars[CB_Q + x], 4);
       mbar_init(&bars[CB_S + x], 1);
       mbar_init(&bars[CB_SF + x], 4);
@@ -203,18 +228,19 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
       mbar_init(&bars[CB_DONE + x], 1);
     }
     mbar_init(&bars[CB_GO], 4);
-    for (int s = 0; s < NFULL; ++s) mbar_init(&full[s], KV8 ? 2 : 1);  // (8 bits: copies, scales)
-    for (int s = 0; s < STG && QK8; ++s) mbar_init(&kfull[s], 1);
-    for (int s = 0; s < STG; ++s) {
+    for (int s = 0; s < KS; ++s) mbar_init(&kfull[s], 1);
+    for (int s = 0; s < NFULL; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < VS; ++s) {
       mbar_init(&ready[s], Cfg::CONV_WARPS);
-      mbar_init(&empty[s], two ? 2 : 1);
+      mbar_init(&vempty[s], two ? 2 : 1);
     }
     for (int s = 0; s < RSTG; ++s) mbar_init(&rawempty[s], Cfg::CONV_WARPS);
+    for (int s = 0; s < 8; ++s) mbar_init(&scales[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
+  if (warp == Cfg::W_MMA) {
+    tmem_alloc(tmem_slot, Cfg::TMEM);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -232,12 +258,9 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
     if (lane == 0) mbar_arrive(bar);
   };
 
-  if (warp >= 8) {
-    // 512 threads start at 128 registers: 256 * 64 + 256 * 192 = 512 * 128;
-    // 384 at 168: 128 * 88 + 256 * 208 = 384 * 168
-    if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
+  if (warp >= Cfg::W_COPY) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::R_REST));
+    if (warp == Cfg::W_COPY) {
       // ============================================================== copies
       if (lane == 0) {
         tma_prefetch_desc(&map_k);
@@ -246,108 +269,113 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
       const int brows = P < 128 ? P : 128, nbox = 128 / brows;  // a lane a box
       bool ok = true;
       int it = 0;
-      auto lookup = [&](int t) {                       // this lane's page of tile t
+      auto lookup = [&](int t) {  // this lane's page of tile t
         const int at = (m0 + t) * 128 + lane * brows;
         if (t >= nt || lane >= nbox || at >= hi || at + brows <= lo) return static_cast<int>(p.num_pages);
         const int v = p.batch.block_table[(int64_t)b * p.batch.max_pages + (at >> p.page_shift)];
         if (v >= 0 && v < p.num_pages) return v;
         report_batch();
-        return static_cast<int>(p.num_pages);          // past the pool: read as zeros
+        return static_cast<int>(p.num_pages);  // past the pool: read as zeros
       };
       int pg_next = lookup(0);
       for (; it < nt; ++it) {
-        const int pg = pg_next;
+        const int pg = pg_next, blk = pg * p.Hkv + g, r = lane * brows, row = ((m0 + it) * 128 + r) & (P - 1);
         float2 sc = make_float2(1.f, 0.f);
         if (KV8 && pg < p.num_pages) {
           const int64_t i = (int64_t)pg * p.Hkv + g;
           sc = make_float2(p.k_scale[i], p.v_scale[i]);
         }
         pg_next = lookup(it + 1);
-        const int s = it % NFULL, st = it % STG;
-        if (it >= NFULL && !wait(KV8 ? &rawempty[s] : &empty[s], (it / NFULL - 1) & 1)) { ok = false; break; }
-        if (QK8 && it >= STG && !wait(&empty[st], (it / STG - 1) & 1)) { ok = false; break; }
+        const int ks = it % KS, s = it % NFULL;
+        // One row tile: V of tile it - RSTG was converted, for which V of tile it -
+        // KS had been multiplied.  K of a tile is done with when its V is.
+        if (NX == 2 && it >= VS && !wait(&vempty[it % VS], (it / VS - 1) & 1)) { ok = false; break; }
+        if (KV8 && it >= RSTG && !wait(&rawempty[s], (it / NFULL - 1) & 1)) { ok = false; break; }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], KV8 ? Cfg::RAWS : 2 * Cfg::TILE);
-          if (QK8) mbar_arrive_expect_tx(&kfull[st], Cfg::KTILE);
+          mbar_arrive_expect_tx(&kfull[ks], Cfg::KTILE);
+          mbar_arrive_expect_tx(&full[s], KV8 ? Cfg::RAW : Cfg::TILE);
         }
         __syncwarp();
         if (lane < nbox) {
-          const int r = lane * brows, row = ((m0 + it) * 128 + r) & (P - 1), blk = pg * p.Hkv + g;
+#pragma unroll
+          for (int pn = 0; pn < (KV8 ? 1 : Cfg::NP); ++pn)
+            tma_load_3d(sm + Cfg::K_OFF + ks * Cfg::KTILE + pn * Cfg::PANEL + r * Cfg::QRB, &map_k, &kfull[ks], pn * (Cfg::RB / 2),
+                        row, blk);
+        }
+        if constexpr (KV8) {
+          // The scales of each 16 positions, under the copy.  (Slot it mod 8 was
+          // last read for tile it - 8, and the softmax is past tile it - KS.)
+          const float2 f = make_float2(exp2i(stored_exponent(sc.x)), static_cast<float>(stored_exponent(sc.y)));
+          if (lane < nbox)
+            for (int i = 0; i < brows / 16; ++i) sc_tile[it % 8 * 8 + lane * (brows / 16) + i] = f;
+          warp_arrive(&scales[it % 8]);
+        }
+        if (lane < nbox) {
           if constexpr (KV8) {
-            unsigned char* raw = sm + Cfg::RAW_OFF + s * Cfg::RAWS + r * HD;
-            if constexpr (QK8) tma_load_3d(sm + Cfg::K_OFF + st * Cfg::KTILE + r * HD, &map_k, &kfull[st], 0, row, blk);
-            else tma_load_3d(raw + Cfg::RAW, &map_k, &full[s], 0, row, blk);
-            tma_load_3d(raw, &map_v, &full[s], 0, row, blk);
+            tma_load_3d(sm + Cfg::RAW_OFF + s * Cfg::RAW + r * HD, &map_v, &full[s], 0, row, blk);
           } else {
 #pragma unroll
-            for (int pn = 0; pn < Cfg::NP; ++pn) {
-              const int at = s * Cfg::TILE + pn * Cfg::PANEL + r * Cfg::RB;
-              tma_load_3d(sm + Cfg::K_OFF + at, &map_k, &full[s], pn * (Cfg::RB / 2), row, blk);
-              tma_load_3d(sm + Cfg::V_OFF + at, &map_v, &full[s], pn * (Cfg::RB / 2), row, blk);
-            }
-          }
-          if constexpr (KV8) {  // the scales of each 16 positions, under the copies
-            const float2 f = make_float2(exp2i(stored_exponent(sc.x)), static_cast<float>(stored_exponent(sc.y)));
-            for (int i = 0; i < brows / 16; ++i) sc_raw[s * 8 + lane * (brows / 16) + i] = f;
+            for (int pn = 0; pn < Cfg::NP; ++pn)
+              tma_load_3d(sm + Cfg::V_OFF + s * Cfg::TILE + pn * Cfg::PANEL + r * Cfg::RB, &map_v, &full[s], pn * (Cfg::RB / 2), row,
+                          blk);
           }
         }
-        if (KV8) warp_arrive(&full[s]);
       }
       if (!ok && lane == 0) {  // copies still in flight after a wait that gave up
         volatile int never = 0;
         for (int i = it > NFULL ? it - NFULL : 0; i < it; ++i) mbar_wait(&full[i % NFULL], (i / NFULL) & 1, &never);
-        for (int i = it > STG ? it - STG : 0; i < it && QK8; ++i) mbar_wait(&kfull[i % STG], (i / STG) & 1, &never);
+        for (int i = it > KS ? it - KS : 0; i < it; ++i) mbar_wait(&kfull[i % KS], (i / KS) & 1, &never);
       }
-    } else if (warp == 9 || (warp == 10 && two)) {
+    } else if (warp == Cfg::W_MMA || (NX == 2 && warp == Cfg::W_MMA + 1 && two)) {
       // ============================================================ products
-      const int x = warp - 9;
-      const uint32_t fmt = KV8 ? 0u : (1u << 7) | (1u << 10);  // operands f16 or bf16
+      const int x = warp - Cfg::W_MMA;
+      const uint32_t fmt = KV8 ? 0u : (1u << 7) | (1u << 10);  // operands e4m3 or f16, or bf16
       const uint32_t idesc_s = (idesc_bf16_f32(128, 128, 0, 0) & ~((7u << 7) | (7u << 10))) | fmt;
       constexpr int NV = Cfg::RB / 2;                          // columns of O a product: one panel of V
       const uint32_t idesc_o = (idesc_bf16_f32(128, NV, 0, 1) & ~((7u << 7) | (7u << 10))) | fmt;
-      const uint64_t dq = smem_desc(smem_u32(sm + Cfg::Q_OFF + x * Cfg::TILE), 16, 8 * Cfg::QRB, Cfg::swz(Cfg::QRB));
+      const uint64_t dq = smem_desc(smem_u32(sm + Cfg::Q_OFF + x * Cfg::QTILE), 16, 8 * Cfg::QRB, Cfg::swz(Cfg::QRB));
       const uint64_t dk = smem_desc(smem_u32(sm + Cfg::K_OFF), 16, 8 * Cfg::QRB, Cfg::swz(Cfg::QRB));
       const uint64_t dv = smem_desc(smem_u32(sm + Cfg::V_OFF), 4096, 8 * Cfg::RB, Cfg::swz(Cfg::RB));
       constexpr uint32_t kTile = Cfg::TILE >> 4, kKTile = Cfg::KTILE >> 4, kPanel = Cfg::PANEL >> 4;
       constexpr int KPP = Cfg::RB / 32;  // steps of 32 bytes a panel
       bool ok = wait(&bars[CB_Q + x], 0);
       auto issue_s = [&](int t) {
-        const int s = t % STG;
-        if constexpr (!KV8)
-          if (!wait(&full[s], (t / STG) & 1)) return false;
-        if (!wait(QK8 ? &kfull[s] : &ready[s], (t / STG) & 1)) return false;
+        const int s = t % KS;
+        if (!wait(&kfull[s], (t / KS) & 1)) return false;
         if (Cfg::AHEAD && t > 0 && !wait(&bars[CB_SF + x], (t - 1) & 1)) return false;  // S(t - 1) was read
         tc_fence_after();
-        if constexpr (QK8) {
+        if constexpr (KV8) {
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {  // the first parts of Q, then the second
-            constexpr int KS = HD / 32;
-            umma_ss8_w(tmem + Cfg::COL_S + 128 * x, dq + k / KS * (Cfg::RAW >> 4) + 2 * (k % KS), dk + s * kKTile + 2 * (k % KS),
-                       idesc_s, k > 0 ? 1u : 0u);
+          for (int k = 0; k < Cfg::KD / 16; ++k) {  // the first parts of Q, then the second
+            constexpr int STEPS = Cfg::KD / 32;
+            umma_ss8_w(tmem + Cfg::COL_S + 128 * x, dq + k / STEPS * kKTile + 2 * (k % STEPS),
+                       dk + s * kKTile + 2 * (k % STEPS), idesc_s, k > 0 ? 1u : 0u);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
             const uint32_t at = k / KPP * kPanel + 2 * (k % KPP);
-            umma_ss_w(tmem + Cfg::COL_S + 128 * x, dq + at, dk + s * kTile + at, idesc_s, k > 0 ? 1u : 0u);
+            umma_ss_w(tmem + Cfg::COL_S + 128 * x, dq + at, dk + s * kKTile + at, idesc_s, k > 0 ? 1u : 0u);
           }
         }
         tc_commit_w(&bars[CB_S + x]);
         return true;
       };
       auto issue_pv = [&](int t) {
-        const int s = t % STG;
+        const int s = t % VS;
+        if constexpr (!KV8)
+          if (!wait(&full[s], (t / VS) & 1)) return false;
+        if (!wait(&ready[s], (t / VS) & 1)) return false;
         if (!wait(&bars[CB_P + x], t & 1)) return false;
-        if (QK8 && !wait(&ready[s], (t / STG) & 1)) return false;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
 #pragma unroll
           for (int pn = 0; pn < Cfg::NP; ++pn)
-            umma_ts_w(tmem + Cfg::COL_O + Cfg::O_STEP * x + pn * NV, tmem + Cfg::COL_P + Cfg::P_STEP * x + 8 * k,
+            umma_ts_w(tmem + Cfg::COL_O + Cfg::STEP * x + pn * NV, tmem + Cfg::COL_P + Cfg::STEP * x + 8 * k,
                       dv + s * kTile + pn * kPanel + k * Cfg::RB, idesc_o, t > 0 || k > 0 ? 1u : 0u);
         tc_commit_w(&bars[CB_O + x]);
-        tc_commit_w(&empty[s]);
+        tc_commit_w(&vempty[s]);
         return true;
       };
       ok = ok && issue_s(0);
@@ -359,38 +387,37 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
       tc_commit_w(&bars[CB_DONE + x]);
       volatile int never = 0;
       mbar_wait(&bars[CB_DONE + x], 0, &never);
-    } else if (warp >= Cfg::CONV_WARP0) {
-      // ======================================== tiles fit to be multiplied
-      const int cw = warp - Cfg::CONV_WARP0;
+    } else if (warp >= Cfg::W_CONV) {
+      // =================================== tiles of V fit to be multiplied
+      const int cw = warp - Cfg::W_CONV;
       for (int t = 0; t < nt; ++t) {
-        const int s = t % STG, k0 = (m0 + t) * 128;
+        const int s = t % VS, k0 = (m0 + t) * 128;
         const bool edge = k0 < lo || k0 + 128 > hi;
         if constexpr (KV8) {
-          const int rs = t % (RSTG > 0 ? RSTG : 1);
-          if (!wait(&full[rs], (t / (RSTG > 0 ? RSTG : 1)) & 1)) break;
-          if (t >= STG && !wait(&empty[s], (t / STG - 1) & 1)) break;
-          const unsigned char* raw = sm + Cfg::RAW_OFF + rs * Cfg::RAWS;
+          constexpr int R = RSTG > 0 ? RSTG : 1;
+          const int rs = t % R;
+          if (!wait(&full[rs], (t / R) & 1)) break;
+          if (t >= VS && !wait(&vempty[s], (t / VS - 1) & 1)) break;
+          const unsigned char* raw = sm + Cfg::RAW_OFF + rs * Cfg::RAW;
           constexpr int CPR = HD / 16;  // 16-code chunks a row
-#pragma unroll 4
-          for (int i = cw * 32 + lane; i < Cfg::RAWS / 16; i += 128) {
-            const bool is_k = i >= 128 * CPR;
-            const int r = (is_k ? i - 128 * CPR : i) / CPR, c = i % CPR;
+#pragma unroll 2
+          for (int i = cw * 32 + lane; i < 128 * CPR; i += 32 * Cfg::CONV_WARPS) {
+            const int r = i / CPR, c = i % CPR;
             uint4 v = *reinterpret_cast<const uint4*>(raw + i * 16);
-            if (edge && !is_k && (k0 + r < lo || k0 + r >= hi)) v = make_uint4(0u, 0u, 0u, 0u);
+            if (edge && (k0 + r < lo || k0 + r >= hi)) v = make_uint4(0u, 0u, 0u, 0u);
             const uint4 a = make_uint4(e4m3x2_to_f16x2(v.x, false), e4m3x2_to_f16x2(v.x, true),
                                        e4m3x2_to_f16x2(v.y, false), e4m3x2_to_f16x2(v.y, true));
             const uint4 d = make_uint4(e4m3x2_to_f16x2(v.z, false), e4m3x2_to_f16x2(v.z, true),
                                        e4m3x2_to_f16x2(v.w, false), e4m3x2_to_f16x2(v.w, true));
-            unsigned char* dst = sm + (is_k ? Cfg::K_OFF : Cfg::V_OFF) + s * Cfg::TILE;
+            unsigned char* dst = sm + Cfg::V_OFF + s * Cfg::TILE;
             *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::RB>(r, 2 * c)) = a;
             *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::RB>(r, 2 * c + 1)) = d;
           }
-          if (cw == 0 && lane < 8) sc_tile[s * 8 + lane] = sc_raw[rs * 8 + lane];
           fence_proxy_async_shared();
           warp_arrive(&ready[s]);
           if (lane == 0) mbar_arrive(&rawempty[rs]);
         } else {
-          if (!wait(&full[s], (t / STG) & 1)) break;
+          if (!wait(&full[s], (t / VS) & 1)) break;
           if (edge) {
             constexpr int CPT = HD / 8;  // 16-byte chunks a row
             for (int i = lane; i < 128 * CPT; i += 32) {
@@ -407,8 +434,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
     }
   } else {
     // ================================================================ softmax
-    if constexpr (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::R_SOFT));
     const int x = warp >> 2, wq = warp & 3, r = wq * 32 + lane;  // row of the tile
     if (x == 0 || two) {
     const bool live = 128 * x + r < nrow;
@@ -419,7 +445,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
     const int64_t at = (int64_t)(sq.row0 + tok) * p.Hq + (live ? h : 0);
     float rowscale = p.scale_log2;
     {  // this row of Q
-      unsigned char* dst = sm + Cfg::Q_OFF + x * Cfg::TILE;
+      unsigned char* dst = sm + Cfg::Q_OFF + x * Cfg::QTILE;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + at * HD);
       if constexpr (KV8) {
         float amax = 0.f;
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
           for (int i = 0; i < 4; ++i)
             amax = chunk_max3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
         }
-        const int ex = min(max(log2i(amax), -60), 126) - (QK8 ? 7 : 0);  // 2^ex <= amax < 2^(ex + 1), or 2^7 of that
+        const int ex = min(max(log2i(amax), -60), 126) - 7;  // 2^7 <= amax 2^-ex < 2^8
         const float by = exp2i(-ex);
         rowscale *= exp2i(ex);
 #pragma unroll
@@ -445,26 +471,22 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
             for (int i = 0; i < 4; ++i)
               f[8 * j + 2 * i] = __uint_as_float(w[i] << 16) * by, f[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * by;
           }
-          if constexpr (QK8) {
-            uint32_t u[4], e[4];
+          uint32_t u[4], e[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              u[i] = to_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-              const uint32_t l2 = e4m3x2_to_f16x2(u[i], false), h2 = e4m3x2_to_f16x2(u[i], true);
-              const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l2));
-              const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              e[i] = to_e4m3x4(f[4 * i] - fl.x, f[4 * i + 1] - fl.y, f[4 * i + 2] - fh.x, f[4 * i + 3] - fh.y);
-            }
-            *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::QRB>(r, c)) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(dst + Cfg::RAW + chunk_off<Cfg::QRB>(r, c)) = make_uint4(e[0], e[1], e[2], e[3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float* q = f + 8 * j;
-              *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::RB>(r, 2 * c + j)) = make_uint4(
-                  chunk_pack<true>(q[0], q[1]), chunk_pack<true>(q[2], q[3]), chunk_pack<true>(q[4], q[5]), chunk_pack<true>(q[6], q[7]));
-            }
+          for (int i = 0; i < 4; ++i) {
+            u[i] = to_e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            const uint32_t l2 = e4m3x2_to_f16x2(u[i], false), h2 = e4m3x2_to_f16x2(u[i], true);
+            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&l2));
+            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            e[i] = to_e4m3x4(f[4 * i] - fl.x, f[4 * i + 1] - fl.y, f[4 * i + 2] - fh.x, f[4 * i + 3] - fh.y);
           }
+          *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::QRB>(r, c)) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(dst + Cfg::KTILE + chunk_off<Cfg::QRB>(r, c)) = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+#pragma unroll
+        for (int c = HD / 16; c < Cfg::KD / 16; ++c) {
+          *reinterpret_cast<uint4*>(dst + chunk_off<Cfg::QRB>(r, c)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + Cfg::KTILE + chunk_off<Cfg::QRB>(r, c)) = make_uint4(0u, 0u, 0u, 0u);
         }
       } else {
 #pragma unroll
@@ -476,8 +498,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
     }
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + Cfg::COL_S + 128 * x;
-    const uint32_t tP = tmem + lane_off + Cfg::COL_P + Cfg::P_STEP * x;
-    const uint32_t tO = tmem + lane_off + Cfg::COL_O + Cfg::O_STEP * x;
+    const uint32_t tP = tmem + lane_off + Cfg::COL_P + Cfg::STEP * x;
+    const uint32_t tO = tmem + lane_off + Cfg::COL_O + Cfg::STEP * x;
     // positions of the tile's first and last row
     const int t_lo = first + (row0 + 128 * x) / p.group, t_hi = first + (row0 + min(nrow, 128 * x + 128) - 1) / p.group;
     const int r_lo = p.window > 0 && pos + 1 > p.window ? static_cast<int>(pos + 1 - p.window) : 0;
@@ -487,58 +509,51 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
     // the two do not reach their exponentials together
     if (x == 1) ok = wait(&bars[CB_GO], 0);
     for (int t = 0; t < nt && ok; ++t) {
-      const int k0 = (m0 + t) * 128, s = t % STG;
+      const int k0 = (m0 + t) * 128;
       const bool need_mask = k0 + 127 > t_lo || (p.window > 0 && k0 <= t_hi - p.window) || nrow < 128 * x + 128;
+      // visible columns [lo_c, lo_c + span]; an empty interval for a row that sees nothing here
+      const int lo_c = max(r_lo - k0, 0), span_i = (live ? pos - k0 : -1) - lo_c;
+      const unsigned span = span_i < 0 ? 0u : static_cast<unsigned>(span_i);
+      const int lo_e = span_i < 0 ? (1 << 20) : lo_c;
+      const float2* tile_sc = sc_tile + t % 8 * 8;
+      // the factor of a group's scores: above zero, so that a masked score stays -inf
+      auto factor_of = [&](float2 f) { return fmaxf(rowscale * f.x, 1.17549435e-38f); };
       if (!wait(&bars[CB_S + x], t & 1)) { ok = false; break; }
+      if constexpr (KV8)
+        if (!wait(&scales[t % 8], (t / 8) & 1)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[128];
-      tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-      tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-      tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-      tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+      float* sc = reinterpret_cast<float*>(sr);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * i]));
       tc_wait_ld();
       tc_fence_before();
       if (Cfg::AHEAD) warp_arrive(&bars[CB_SF + x]);
-      float* sc = reinterpret_cast<float*>(sr);
       if (need_mask) {
-        // visible columns [lo_c, lo_c + span]; an empty interval for a row that sees nothing here
-        const int lo_c = max(r_lo - k0, 0), hi_c = live ? pos - k0 : -1;
-        const int span_i = hi_c - lo_c;
-        const unsigned span = span_i < 0 ? 0u : static_cast<unsigned>(span_i);
-        const int lo_e = span_i < 0 ? (1 << 20) : lo_c;
 #pragma unroll
         for (int c = 0; c < 128; ++c) sc[c] = (unsigned)(c - lo_e) <= span ? sc[c] : -INFINITY;
       }
-      // the row's maximum; 8 bits: of each 16 positions, scaled, then of those
-      float m_tile;
-      if constexpr (KV8) {
-        if (!wait(&ready[s], (t / STG) & 1)) { ok = false; break; }  // (passed long ago: orders the scales' reads)
-        m_tile = -INFINITY;
+      // the row's maximum; 8 bits: of each SPAN positions, scaled, then of those
+      float m_tile = -INFINITY;
+      constexpr int G = KV8 ? SPAN : 64;  // positions of one factor
 #pragma unroll
-        for (int q = 0; q < 128 / SPAN; ++q) {
-          const float2 f = sc_tile[s * 8 + q * (SPAN / 16)];
-          const float ga = fmaxf(rowscale * f.x, 1.17549435e-38f);  // above zero, so that a masked score stays -inf
-          float m4[4];
+      for (int q = 0; q < 128 / G; ++q) {
+        float m4[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = SPAN * q + i;
-            m4[i] = chunk_max3(sc[c], sc[c + 4], sc[c + 8]);
+        for (int i = 0; i < 4; ++i) {
+          const int c = G * q + i;
+          m4[i] = chunk_max3(sc[c], sc[c + 4], sc[c + 8]);
 #pragma unroll
-            for (int j = 12; j < SPAN - 4; j += 8) m4[i] = chunk_max3(m4[i], sc[c + j], sc[c + j + 4]);
-            m4[i] = fmaxf(m4[i], sc[c + SPAN - 4]);
-          }
-          m_tile = fmaxf(m_tile, fmaf(fmaxf(chunk_max3(m4[0], m4[1], m4[2]), m4[3]), ga, f.y));
+          for (int j = 12; j < G - 4; j += 8) m4[i] = chunk_max3(m4[i], sc[c + j], sc[c + j + 4]);
+          m4[i] = fmaxf(m4[i], sc[c + G - 4]);
         }
-      } else {
-        float m8[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float m = chunk_max3(sc[q], sc[q + 8], sc[q + 16]);
-#pragma unroll
-          for (int c = 24; c < 120; c += 16) m = chunk_max3(m, sc[c + q], sc[c + 8 + q]);
-          m8[q] = fmaxf(m, sc[120 + q]);
+        const float mq = fmaxf(chunk_max3(m4[0], m4[1], m4[2]), m4[3]);
+        if constexpr (KV8) {
+          const float2 f = tile_sc[q * SPAN / 16];
+          m_tile = fmaxf(m_tile, fmaf(mq, factor_of(f), f.y));
+        } else {
+          m_tile = fmaxf(m_tile, mq * rowscale);
         }
-        m_tile = fmaxf(chunk_max3(chunk_max3(m8[0], m8[1], m8[2]), chunk_max3(m8[3], m8[4], m8[5]), m8[6]), m8[7]) * rowscale;
       }
       float factor = 1.f;
       bool rescale = false;
@@ -548,10 +563,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
         rescale = true;
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;
-      if (t > 0) {  // the last product still reads P and O
-        if (!wait(&bars[CB_O + x], (t - 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-      }
       float sum = 0.f;
       f2 acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)}, a2 = pk2(rowscale, rowscale), c2 = pk2(-m_use, -m_use);
       float inv = 1.f;  // 1 / value scale of the group
@@ -562,8 +573,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
         for (int j = 0; j < 16; ++j) {
           const int c = 32 * k + 2 * j;
           if (KV8 && c % SPAN == 0) {
-            const float2 f = sc_tile[s * 8 + c / 16];
-            const float ga = fmaxf(rowscale * f.x, 1.17549435e-38f);
+            const float2 f = tile_sc[c / 16];
+            const float ga = factor_of(f);
             a2 = pk2(ga, ga);
             c2 = pk2(f.y - m_use, f.y - m_use);
             inv = exp2i(-static_cast<int>(f.y));
@@ -577,6 +588,10 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
             sum = fmaf(tot.x + tot.y, inv, sum);
             acc[0] = acc[1] = pk2(0.f, 0.f);
           }
+        }
+        if (k == 0 && t > 0) {  // until here the last product may read P and O
+          ok = wait(&bars[CB_O + x], (t - 1) & 1);
+          tc_fence_after();
         }
         tmem_st16(tP + 16 * k, pk);
       }
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
       tc_wait_st();
       tc_fence_before();
       warp_arrive(&bars[CB_P + x]);
-      if (t == 0 && x == 0 && lane == 0) mbar_arrive(&bars[CB_GO]);
+      if (NX == 2 && t == 0 && x == 0 && lane == 0) mbar_arrive(&bars[CB_GO]);
     }
     if (ok && wait(&bars[CB_O + x], (nt - 1) & 1)) {
       tc_fence_after();
@@ -632,9 +647,9 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == Cfg::W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, Cfg::TMEM);
   }
 }
 
@@ -654,16 +669,17 @@ static int chunk_go(const samba_paged_attn_args& a, const PagedPlan& pl, cudaStr
   CUtensorMap mk, mv;
   const uint64_t dims[3] = {(uint64_t)HD, (uint64_t)P, (uint64_t)a.kv.num_pages * a.kv.heads_kv};
   const uint64_t strides[2] = {(uint64_t)HD * el, (uint64_t)HD * el * P};
-  const uint32_t box[3] = {(uint32_t)(KV8 ? HD : Cfg::RB / 2), (uint32_t)std::min(P, 128), 1u};
+  const uint32_t box_k[3] = {(uint32_t)(KV8 ? Cfg::KD : Cfg::RB / 2), (uint32_t)std::min(P, 128), 1u};
+  const uint32_t box_v[3] = {(uint32_t)(KV8 ? HD : Cfg::RB / 2), (uint32_t)std::min(P, 128), 1u};
   auto swizzle = [](int rb) {
     return rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : rb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
   };
-  const CUtensorMapSwizzle swk = KV8 && !Cfg::QK8 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle(Cfg::QRB);
+  const CUtensorMapSwizzle swk = swizzle(Cfg::QRB);
   const CUtensorMapSwizzle swv = KV8 ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle(Cfg::RB);
   const CUtensorMapDataType dt = KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  int rc = encode_tiled(&mk, dt, 3, a.kv.k, dims, strides, box, swk, "samba_paged_attn K pool");
+  int rc = encode_tiled(&mk, dt, 3, a.kv.k, dims, strides, box_k, swk, "samba_paged_attn K pool");
   if (rc) return rc;
-  rc = encode_tiled(&mv, dt, 3, a.kv.v, dims, strides, box, swv, "samba_paged_attn V pool");
+  rc = encode_tiled(&mv, dt, 3, a.kv.v, dims, strides, box_v, swv, "samba_paged_attn V pool");
   if (rc) return rc;
   ChunkParams p;
   p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
