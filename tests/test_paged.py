@@ -217,6 +217,23 @@ def test_attention_matches_its_definition(case, e4m3):
     check_attn(c, window, run_attn(c, window))
 
 
+MANY = [
+    # new, past, Hq, Hkv, d, P, window: rows and heads enough that no key tiles are split off
+    ([130] * 9, [1700, 1500, 0, 1601, 1024, 900, 1151, 1407, 1279], 18, 18, 64, 64, 0),
+    ([129] * 9, [1200] * 9, 18, 18, 16, 16, 0),
+    ([257] * 9, [1300] * 9, 18, 18, 128, 128, 1200),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"d{c[4]}_p{c[5]}_w{c[6]}")
+def test_attention_over_many_key_tiles(case, e4m3):
+    """More key tiles a block than any of its rings holds."""
+    new, past, Hq, Hkv, d, P, window = case
+    c = Case(new, past, Hq, Hkv, d, P, e4m3, seed=5 + d, slack=2)
+    check_attn(c, window, run_attn(c, window))
+
+
 LOOSE = [
     # new, past, Hq, Hkv, d, P, window, max_kv
     ([1], [0], 4, 2, 64, 16, 0, 400000),
