@@ -11,12 +11,12 @@
 // 8 bits, up to a head dimension of 64: a block has one row tile and half of an
 // SM's tensor and shared memory, so two blocks share an SM.  One's start and end
 // fall under the other's exponentials, and the last round of units leaves less idle
-// (4 sequences of 1536 rows, 32 heads, windows of 2048: 118 us, two tiles a block
-// 130; 8192 rows: 474 and 519).
+// (5 sequences of 200 to 1500 new tokens, 32 heads: 114 us, two tiles a block
+// 130; 8192 rows: 456 and 519).
 //
 // bf16, or a head dimension of 128, whose tiles do not fit twice: a block has two
 // row tiles that share its keys (bf16, head dimension 64, 4736 rows of 32 heads:
-// 136 us, 147 with a tile a block, which copies the keys twice as often).  With
+// 135 us, 147 with a tile a block, which copies the keys twice as often).  With
 // 128 P takes the place of S, and S of the next key tile waits for P V.
 //
 // Four warps a row tile are its softmax, a thread a row: they bring their rows of
@@ -116,6 +116,19 @@ __device__ __forceinline__ float chunk_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Whether the phase is over, asked ahead of a wait so that the answer is there by
+// then (a wait that need not wait still took 200 clocks of a key tile's 3000).
+__device__ __forceinline__ bool chunk_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t chunk_pack(float lo, float hi) {
   uint32_t r;
@@ -171,16 +184,15 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
   using Cfg = ChunkCfg<HD, KV8>;
   constexpr int NX = Cfg::NX, KS = Cfg::KS, VS = Cfg::VS, RSTG = Cfg::RSTG, NFULL = Cfg::NFULL;
   static_assert(NX == 2 || KV8, "the copies' waits");
-  static_assert(CB_STAGE + KS + NFULL + 2 * VS + RSTG + 8 <= 62, "barrier block");
+  static_assert(CB_STAGE + KS + NFULL + 2 * VS + RSTG <= 62, "barrier block");
   extern __shared__ unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);  // (an offset: still known as shared memory)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::BAR_OFF);
-  uint64_t* kfull = bars + CB_STAGE;    // [KS] a tile of K landed
+  uint64_t* kfull = bars + CB_STAGE;    // [KS] a tile of K landed (8 bits: and its scales were written)
   uint64_t* full = kfull + KS;          // [NFULL] a tile of V landed
   uint64_t* ready = full + NFULL;       // [VS] it may be multiplied
   uint64_t* vempty = ready + VS;        // [VS] its products are done
   uint64_t* rawempty = vempty + VS;     // [RSTG] its codes were converted
-  uint64_t* scales = rawempty + RSTG;   // [8] 8 bits: the scales of a tile (slot t mod 8) are there
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 62);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* sc_tile = reinterpret_cast<float2*>(sm + Cfg::SC_OFF);  // [8][8] key scale, value scale exponent
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
   if (threadIdx.x == 0) {
     for (int x = 0; x < NX; ++x) {
       mbar_init(&bars[CB_Q + x], 4);
-      mbar_init(&bars[CB_S + x], 1);
+      mbar_init(&bars[CB_S + x], KV8 ? 2 : 1);
       mbar_init(&bars[CB_SF + x], 4);
       mbar_init(&bars[CB_P + x], 4);
       mbar_init(&bars[CB_O + x], 1);
@@ -235,7 +247,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
       mbar_init(&vempty[s], two ? 2 : 1);
     }
     for (int s = 0; s < RSTG; ++s) mbar_init(&rawempty[s], Cfg::CONV_WARPS);
-    for (int s = 0; s < 8; ++s) mbar_init(&scales[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -277,20 +288,29 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
         report_batch();
         return static_cast<int>(p.num_pages);  // past the pool: read as zeros
       };
-      int pg_next = lookup(0);
+      auto scales_of = [&](int pg) {
+        if (!KV8 || pg >= p.num_pages) return make_float2(1.f, 0.f);
+        const int64_t i = (int64_t)pg * p.Hkv + g;
+        return make_float2(p.k_scale[i], p.v_scale[i]);
+      };
+      int pg = lookup(0);
+      float2 sc = scales_of(pg);
       for (; it < nt; ++it) {
-        const int pg = pg_next, blk = pg * p.Hkv + g, r = lane * brows, row = ((m0 + it) * 128 + r) & (P - 1);
-        float2 sc = make_float2(1.f, 0.f);
-        if (KV8 && pg < p.num_pages) {
-          const int64_t i = (int64_t)pg * p.Hkv + g;
-          sc = make_float2(p.k_scale[i], p.v_scale[i]);
-        }
-        pg_next = lookup(it + 1);
+        const int blk = pg * p.Hkv + g, r = lane * brows, row = ((m0 + it) * 128 + r) & (P - 1);
+        pg = lookup(it + 1);
         const int ks = it % KS, s = it % NFULL;
         // One row tile: V of tile it - RSTG was converted, for which V of tile it -
         // KS had been multiplied.  K of a tile is done with when its V is.
         if (NX == 2 && it >= VS && !wait(&vempty[it % VS], (it / VS - 1) & 1)) { ok = false; break; }
         if (KV8 && it >= RSTG && !wait(&rawempty[s], (it / NFULL - 1) & 1)) { ok = false; break; }
+        if constexpr (KV8) {
+          // The scales of each 16 positions.  (Slot it mod 8 was last read for tile
+          // it - 8, and the softmax is past tile it - KS.)
+          const float2 f = make_float2(exp2i(stored_exponent(sc.x)), static_cast<float>(stored_exponent(sc.y)));
+          if (lane < nbox)
+            for (int i = 0; i < brows / 16; ++i) sc_tile[it % 8 * 8 + lane * (brows / 16) + i] = f;
+          __syncwarp();
+        }
         if (lane == 0) {
           mbar_arrive_expect_tx(&kfull[ks], Cfg::KTILE);
           mbar_arrive_expect_tx(&full[s], KV8 ? Cfg::RAW : Cfg::TILE);
@@ -302,14 +322,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
             tma_load_3d(sm + Cfg::K_OFF + ks * Cfg::KTILE + pn * Cfg::PANEL + r * Cfg::QRB, &map_k, &kfull[ks], pn * (Cfg::RB / 2),
                         row, blk);
         }
-        if constexpr (KV8) {
-          // The scales of each 16 positions, under the copy.  (Slot it mod 8 was
-          // last read for tile it - 8, and the softmax is past tile it - KS.)
-          const float2 f = make_float2(exp2i(stored_exponent(sc.x)), static_cast<float>(stored_exponent(sc.y)));
-          if (lane < nbox)
-            for (int i = 0; i < brows / 16; ++i) sc_tile[it % 8 * 8 + lane * (brows / 16) + i] = f;
-          warp_arrive(&scales[it % 8]);
-        }
         if (lane < nbox) {
           if constexpr (KV8) {
             tma_load_3d(sm + Cfg::RAW_OFF + s * Cfg::RAW + r * HD, &map_v, &full[s], 0, row, blk);
@@ -320,6 +332,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
                           blk);
           }
         }
+        sc = scales_of(pg);
       }
       if (!ok && lane == 0) {  // copies still in flight after a wait that gave up
         volatile int never = 0;
@@ -359,6 +372,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           }
         }
         tc_commit_w(&bars[CB_S + x]);
+        if (KV8 && lane == 0) mbar_arrive(&bars[CB_S + x]);  // passes the scales on to the softmax
         return true;
       };
       auto issue_pv = [&](int t) {
@@ -508,7 +522,11 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
     // the second tile begins once the first has written its first P, so that
     // the two do not reach their exponentials together
     if (x == 1) ok = wait(&bars[CB_GO], 0);
+    bool s_ready = false;  // S of the coming tile was seen to be there
+    auto wait_after = [&](bool seen, uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, seen) || wait(bar, parity); };
     for (int t = 0; t < nt && ok; ++t) {
+      if (!wait_after(s_ready, &bars[CB_S + x], t & 1)) { ok = false; break; }
+      tc_fence_after();
       const int k0 = (m0 + t) * 128;
       const bool need_mask = k0 + 127 > t_lo || (p.window > 0 && k0 <= t_hi - p.window) || nrow < 128 * x + 128;
       // visible columns [lo_c, lo_c + span]; an empty interval for a row that sees nothing here
@@ -518,10 +536,6 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
       const float2* tile_sc = sc_tile + t % 8 * 8;
       // the factor of a group's scores: above zero, so that a masked score stays -inf
       auto factor_of = [&](float2 f) { return fmaxf(rowscale * f.x, 1.17549435e-38f); };
-      if (!wait(&bars[CB_S + x], t & 1)) { ok = false; break; }
-      if constexpr (KV8)
-        if (!wait(&scales[t % 8], (t / 8) & 1)) { ok = false; break; }
-      tc_fence_after();
       uint32_t sr[128];
       float* sc = reinterpret_cast<float*>(sr);
 #pragma unroll
@@ -563,6 +577,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
         rescale = true;
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;
+      const bool o_done = t > 0 && chunk_test(&bars[CB_O + x], (t - 1) & 1);
       float sum = 0.f;
       f2 acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)}, a2 = pk2(rowscale, rowscale), c2 = pk2(-m_use, -m_use);
       float inv = 1.f;  // 1 / value scale of the group
@@ -590,7 +605,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           }
         }
         if (k == 0 && t > 0) {  // until here the last product may read P and O
-          ok = wait(&bars[CB_O + x], (t - 1) & 1);
+          ok = wait_after(o_done, &bars[CB_O + x], (t - 1) & 1);
           tc_fence_after();
         }
         tmem_st16(tP + 16 * k, pk);
@@ -611,6 +626,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           tmem_st16(tO + 16 * q, o);
         }
       }
+      s_ready = Cfg::AHEAD && chunk_test(&bars[CB_S + x], (t + 1) & 1);
       tc_wait_st();
       tc_fence_before();
       warp_arrive(&bars[CB_P + x]);
