@@ -11,8 +11,8 @@
 // 8 bits, up to a head dimension of 64: a block has one row tile and half of an
 // SM's tensor and shared memory, so two blocks share an SM.  One's start and end
 // fall under the other's exponentials, and the last round of units leaves less idle
-// (5 sequences of 200 to 1500 new tokens, 32 heads: 114 us, two tiles a block
-// 130; 8192 rows: 456 and 519).
+// (5 sequences of 200 to 1500 new tokens, 32 heads: 112 us, two tiles a block
+// 130; 8192 rows: 445 and 519).
 //
 // bf16, or a head dimension of 128, whose tiles do not fit twice: a block has two
 // row tiles that share its keys (bf16, head dimension 64, 4736 rows of 32 heads:
@@ -73,8 +73,8 @@ struct ChunkCfg {
   static constexpr int SMEM = SC_OFF + (KV8 ? 512 : 0) + 1024;
   static constexpr int swz(int rb) { return rb == 128 ? 2 : rb == 64 ? 4 : 6; }  // descriptors' swizzle codes
   // Of each eight pairs of probabilities, so many go to the FMA pipe (bf16, 64,
-  // 4736 rows: 1 of them 141 us, 2 139; a tile a block: 1 121 us, none 118)
-  static constexpr int POLY = NX == 1 ? 0 : HD == 128 ? 1 : 2;
+  // 4736 rows: 1 of them 139 us, 2 135; 8 bits: none 156, 1 155)
+  static constexpr int POLY = KV8 || HD == 128 ? 1 : 2;
   // warps: softmax, copies, products (one a row tile), V
   static constexpr int W_COPY = 4 * NX, W_MMA = W_COPY + 1, CONV_WARPS = !KV8 ? 1 : NX == 1 ? 2 : 4;
   static constexpr int WARPS = W_COPY + (KV8 && NX == 2 ? 8 : 4), W_CONV = WARPS - CONV_WARPS;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           if (t >= VS && !wait(&vempty[s], (t / VS - 1) & 1)) break;
           const unsigned char* raw = sm + Cfg::RAW_OFF + rs * Cfg::RAW;
           constexpr int CPR = HD / 16;  // 16-code chunks a row
-#pragma unroll 2
+#pragma unroll 1
           for (int i = cw * 32 + lane; i < 128 * CPR; i += 32 * Cfg::CONV_WARPS) {
             const int r = i / CPR, c = i % CPR;
             uint4 v = *reinterpret_cast<const uint4*>(raw + i * 16);
@@ -541,8 +541,13 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * i]));
       tc_wait_ld();
-      tc_fence_before();
-      if (Cfg::AHEAD) warp_arrive(&bars[CB_SF + x]);
+      auto read_done = [&] {
+        tc_fence_before();
+        if (Cfg::AHEAD) warp_arrive(&bars[CB_SF + x]);
+      };
+      // S of the next tile is early enough either way: with 8 bits told after the
+      // maximum (112 us, 114 before it), with bf16 before (401 us, 406 after)
+      if constexpr (!KV8) read_done();
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < 128; ++c) sc[c] = (unsigned)(c - lo_e) <= span ? sc[c] : -INFINITY;
@@ -569,6 +574,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           m_tile = fmaxf(m_tile, mq * rowscale);
         }
       }
+      if constexpr (KV8) read_done();
       float factor = 1.f;
       bool rescale = false;
       if (m_tile > m_run + 8.f) {
