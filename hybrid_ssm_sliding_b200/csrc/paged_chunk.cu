@@ -610,9 +610,13 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
             acc[0] = acc[1] = pk2(0.f, 0.f);
           }
         }
-        if (k == 0 && t > 0) {  // until here the last product may read P and O
-          ok = wait_after(o_done, &bars[CB_O + x], (t - 1) & 1);
-          tc_fence_after();
+        if (k == 0) {  // until here the last product may read P and O
+          if (t > 0) {
+            ok = wait_after(o_done, &bars[CB_O + x], (t - 1) & 1);
+            tc_fence_after();
+          } else {
+            __syncwarp();  // (as the vote in a wait: the store below is the whole warp's)
+          }
         }
         tmem_st16(tP + 16 * k, pk);
       }
@@ -646,21 +650,23 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
 #pragma unroll
       for (int q = 0; q < HD / 16; ++q) {
         uint32_t o[16];
+        __syncwarp();  // lanes without a row have stored nothing; the load is the whole warp's
         tmem_ld16(tO + 16 * q, o);
         tc_wait_ld();
-        if (!store) continue;
-        if (p.nsplit == 1) {
-          uint32_t v[8];
+        if (store) {
+          if (p.nsplit == 1) {
+            uint32_t v[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            v[c] = chunk_pack<false>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(p.o + at * HD + 16 * q);
-          dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
-        } else {
+            for (int c = 0; c < 8; ++c)
+              v[c] = chunk_pack<false>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+            uint4* dst = reinterpret_cast<uint4*>(p.o + at * HD + 16 * q);
+            dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 16; c += 2)
-            *reinterpret_cast<float2*>(part + 2 + 16 * q + c) = make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1]));
+            for (int c = 0; c < 16; c += 2)
+              *reinterpret_cast<float2*>(part + 2 + 16 * q + c) = make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1]));
+          }
         }
       }
       if (store && p.nsplit > 1) *reinterpret_cast<float2*>(part) = make_float2(m_run, l_run);
