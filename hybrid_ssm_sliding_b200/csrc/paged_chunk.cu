@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
       auto issue_s = [&](int t) {
         const int s = t % KS;
         if (!wait(&kfull[s], (t / KS) & 1)) return false;
-        if (Cfg::AHEAD && t > 0 && !wait(&bars[CB_SF + x], (t - 1) & 1)) return false;  // S(t - 1) was read
+        // S(t - 1) was read, or with P in its place, the products of that P are done
+        // (one product is not ordered behind another that reads what it writes)
+        if (t > 0 && !wait(&bars[(Cfg::AHEAD ? CB_SF : CB_O) + x], (t - 1) & 1)) return false;
         tc_fence_after();
         if constexpr (KV8) {
 #pragma unroll

@@ -38,3 +38,14 @@ def test_chunk_tiles_that_end_inside_a_warp(case, e4m3):
     o = run_attn(c, 0)
     check_attn(c, 0, o)
     assert all(torch.equal(run_attn(c, 0), o) for _ in range(3))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [0, 700])
+def test_wide_heads_where_scores_and_weights_share_columns(e4m3, window):
+    """A head dimension of 128: the next key tile's scores go where the weights
+    of this one are being multiplied.  Many tiles, two chains a block, no splits."""
+    c = Case([140] * 20, [1024 + 37 * i for i in range(20)], 16, 8, 128, 64, e4m3, seed=95)
+    o = run_attn(c, window)
+    check_attn(c, window, o)
+    assert all(torch.equal(run_attn(c, window), o) for _ in range(5))
