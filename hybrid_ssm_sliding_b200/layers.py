@@ -272,12 +272,15 @@ def paged_swa_layer(hidden, w: SwaLayerWeights, cache, batch, freqs=None, interl
     T, dm = hidden.shape
     Hq, Hkv, d = w.heads_q, w.heads_kv, w.head_dim
     nq, nk = Hq * d, Hkv * d
-    qkv = ops.gemm(hidden, w.qkv_proj, outs=[(torch.empty((T, nq + 2 * nk), dtype=torch.bfloat16, device=hidden.device), 0,
-                                              nq + 2 * nk, None)], workspace=gemm_ws, stream=stream)[0]
-    q, k, v = qkv[:, :nq].unflatten(1, (Hq, d)), qkv[:, nq:nq + nk].unflatten(1, (Hkv, d)), qkv[:, nq + nk:].unflatten(1, (Hkv, d))
-    q = ops.kv_append(q, k, v, cache, batch, freqs=freqs, interleaved=interleaved, stream=stream)
-    o = ops.paged_attn(q, cache, batch, window=w.window, workspace=workspace, stream=stream)
-    return ops.gemm(o.view(T, nq), w.o_proj, workspace=gemm_ws, stream=stream)
+    with ops._here(hidden.get_device(), stream):  # what is allocated on the way is that stream's
+        qkv = ops.gemm(hidden, w.qkv_proj, outs=[(torch.empty((T, nq + 2 * nk), dtype=torch.bfloat16, device=hidden.device),
+                                                  0, nq + 2 * nk, None)], workspace=gemm_ws)[0]
+        q, k, v = (t.unflatten(1, (-1, d)) for t in (qkv[:, :nq], qkv[:, nq:nq + nk], qkv[:, nq + nk:]))
+        q = ops.kv_append(q, k, v, cache, batch, freqs=freqs, interleaved=interleaved)
+        o = ops.paged_attn(q, cache, batch, window=w.window, workspace=workspace)
+        out = ops.gemm(o.view(T, nq), w.o_proj, workspace=gemm_ws)
+    ops._lend(stream, out)
+    return out
 
 
 @dataclass
@@ -298,11 +301,13 @@ def paged_stack(r, blocks, w_final, caches, batch, freqs=None, interleaved=False
     rms(layer(n)) * w_post to r, n being the normed stream; the norm before
     the next block comes in the same pass.  Returns (r, n): the stream and its
     norm with w_final [d_model] fp32."""
-    _, n = ops.block_norm_fwd(r, blocks[0].w_pre, eps=eps, n_dtype=torch.bfloat16, stream=stream)
-    for i, (w, cache) in enumerate(zip(blocks, caches, strict=True)):
-        y = paged_swa_layer(n, w.layer, cache, batch, freqs=freqs, interleaved=interleaved, workspace=workspace,
-                            gemm_ws=gemm_ws, stream=stream)
-        gate = None if w.gate_proj is None else ops.gemm(n, w.gate_proj, workspace=gemm_ws, stream=stream)
-        after = blocks[i + 1].w_pre if i + 1 < len(blocks) else w_final
-        r, n = ops.block_norm_fwd(r, after, y=y, w_post=w.w_post, gate=gate, alpha=w.alpha, eps=eps, stream=stream)
+    with ops._here(r.get_device(), stream):
+        _, n = ops.block_norm_fwd(r, blocks[0].w_pre, eps=eps, n_dtype=torch.bfloat16)
+        for i, (w, cache) in enumerate(zip(blocks, caches, strict=True)):
+            y = paged_swa_layer(n, w.layer, cache, batch, freqs=freqs, interleaved=interleaved, workspace=workspace,
+                                gemm_ws=gemm_ws)
+            gate = None if w.gate_proj is None else ops.gemm(n, w.gate_proj, workspace=gemm_ws)
+            after = blocks[i + 1].w_pre if i + 1 < len(blocks) else w_final
+            r, n = ops.block_norm_fwd(r, after, y=y, w_post=w.w_post, gate=gate, alpha=w.alpha, eps=eps)
+    ops._lend(stream, r, n)
     return r, n

@@ -440,10 +440,15 @@ def _all_same(named, dev):
 
 
 def _here(dev, stream):
-    """A guard that makes device number ``dev`` current; refuses another device's stream."""
-    if stream is not None and stream.device.index != dev:
+    """A guard that makes device number ``dev`` and ``stream`` (if one is given)
+    current; refuses another device's stream.  What is allocated inside comes from
+    that stream's memory: its earlier users are in the stream's own order, which
+    those of the caller's current stream are not."""
+    if stream is None:
+        return _NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-    return _NO_GUARD if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return torch.cuda.stream(stream)
 
 
 _NO_GUARD = contextlib.nullcontext()
@@ -451,12 +456,13 @@ _SIZE_MAX = ctypes.c_size_t(-1).value
 
 
 def _lend(stream, *tensors):
-    """Memory allocated here for a call on another stream than the current one
-    is kept until that stream has passed the call."""
+    """Outputs allocated on another stream (under _here's guard) go to the caller, whose
+    current stream is kept in mind when their memory is given back.  Called
+    outside the guard."""
     if stream is not None:
         for t in tensors:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 class PagedKv:
@@ -576,16 +582,17 @@ def kv_append(q, k, v, cache, batch, freqs=None, interleaved=False, q_out=None, 
         rot = 2 * freqs.numel()
         if freqs.dim() != 1 or rot < 1:
             raise ValueError("freqs must be [rot / 2]")
+    fresh = q is not None and q_out is None
     with _here(dev, stream):
-        if q is not None and q_out is None:
+        if fresh:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            _lend(stream, q_out)
-        if rows == 0 or batch.args.batch == 0:
-            return q_out
-        a = L.KvAppendArgs(L.ptr(q), k.data_ptr(), v.data_ptr(), L.ptr(q_out), L.ptr(freqs), ldq, ldk, ldv, heads_q,
-                           rot, 1 if interleaved else 0, kv, batch.args)
-        a.batch.rows = rows
-        L.check(L.load().samba_kv_append(ctypes.byref(a), L.stream_handle(stream)))
+        if rows > 0 and batch.args.batch > 0:
+            a = L.KvAppendArgs(L.ptr(q), k.data_ptr(), v.data_ptr(), L.ptr(q_out), L.ptr(freqs), ldq, ldk, ldv, heads_q,
+                               rot, 1 if interleaved else 0, kv, batch.args)
+            a.batch.rows = rows
+            L.check(L.load().samba_kv_append(ctypes.byref(a), L.stream_handle(stream)))
+    if fresh:
+        _lend(stream, q_out)
     return q_out
 
 
@@ -614,23 +621,23 @@ def paged_attn(q, cache, batch, window=0, scale=None, o=None, workspace=None, st
         _same(o, "o", torch.bfloat16, shape, dev)
     if workspace is not None:
         _same(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    fresh = o is None
     with _here(dev, stream):
         lib = L.load()
-        if o is None:
+        if fresh:
             o = torch.empty_like(q)
-            _lend(stream, o)
-        if rows == 0 or batch.args.batch == 0:
-            return o
-        a = L.PagedAttnArgs(q.data_ptr(), o.data_ptr(), heads, float(scale) if scale else 0.0, int(window),
-                            L.ptr(workspace), 0 if workspace is None else workspace.numel(), kv, batch.args)
-        a.batch.rows = rows
-        if workspace is None:
-            n = lib.samba_paged_attn_workspace_size(ctypes.byref(a))
-            if 0 < n < _SIZE_MAX:  # otherwise none is needed, or the call says what is wrong
-                workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
-                _lend(stream, workspace)
-                a.workspace, a.workspace_bytes = workspace.data_ptr(), n
-        L.check(lib.samba_paged_attn(ctypes.byref(a), L.stream_handle(stream)))
+        if rows > 0 and batch.args.batch > 0:
+            a = L.PagedAttnArgs(q.data_ptr(), o.data_ptr(), heads, float(scale) if scale else 0.0, int(window),
+                                L.ptr(workspace), 0 if workspace is None else workspace.numel(), kv, batch.args)
+            a.batch.rows = rows
+            if workspace is None:
+                n = lib.samba_paged_attn_workspace_size(ctypes.byref(a))
+                if 0 < n < _SIZE_MAX:  # otherwise none is needed, or the call says what is wrong
+                    workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+                    a.workspace, a.workspace_bytes = workspace.data_ptr(), n
+            L.check(lib.samba_paged_attn(ctypes.byref(a), L.stream_handle(stream)))
+    if fresh:
+        _lend(stream, o)
     return o
 
 
@@ -682,13 +689,12 @@ def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, ep
     if r_out is not None or n is not None or rstd_pre is not None or rstd_post is not None:
         _all_same(((r_out, "r_out", r.dtype, shape), (n, "n", ydt, shape), (rstd_pre, "rstd_pre", f32, (M,)),
                    (rstd_post, "rstd_post", f32, (M,))), dev)
+    fresh_r, fresh_n = y is not None and r_out is None, w_pre is not None and n is None
     with _here(dev, stream):
-        if y is not None and r_out is None:
+        if fresh_r:
             r_out = torch.empty_like(r)
-            _lend(stream, r_out)
-        if w_pre is not None and n is None:
+        if fresh_n:
             n = torch.empty_like(r, dtype=ydt) if y is None else torch.empty_like(y)
-            _lend(stream, n)
         if M > 0:
             a = L.BlockNormArgs(
                 r.data_ptr(), None if y is None else y.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
@@ -697,6 +703,7 @@ def block_norm_fwd(r, w_pre=None, y=None, w_post=None, gate=None, alpha=None, ep
                 None if n is None else n.data_ptr(), None if rstd_pre is None else rstd_pre.data_ptr(),
                 None if rstd_post is None else rstd_post.data_ptr(), M, C, rcode, ycode, eps)
             L.check(L.load().samba_block_norm_fwd(ctypes.byref(a), L.stream_handle(stream)))
+    _lend(stream, r_out if fresh_r else None, n if fresh_n else None)
     return (r if y is None else r_out), n
 
 
@@ -742,18 +749,17 @@ def block_norm_bwd(dn, r, w_pre=None, rstd_pre=None, dr_out=None, y=None, w_post
             for t in (dw_pre, dw_post, dalpha):
                 if t is not None:
                     t.zero_()
-            return out
-        if workspace is None:
-            workspace = empty((max(block_norm_bwd_workspace_size(M, C), 16),), dtype=torch.uint8, device=r.device)
-            _lend(stream, workspace)
-        _lend(stream, *out.values())
-        p = L.ptr
-        a = L.BlockNormBwdArgs(p(dn), p(dr_out), r.data_ptr(), None if dn is None else w_pre.data_ptr(),
-                               None if dn is None else rstd_pre.data_ptr(), p(y), p(w_post),
-                               None if w_post is None else rstd_post.data_ptr(), p(gate), p(alpha), dr.data_ptr(), p(dy),
-                               p(dgate), p(dw_pre), p(dw_post), p(dalpha), workspace.data_ptr(), workspace.numel(), M, C,
-                               rcode, ycode)
-        L.check(L.load().samba_block_norm_bwd(ctypes.byref(a), L.stream_handle(stream)))
+        else:
+            if workspace is None:
+                workspace = empty((max(block_norm_bwd_workspace_size(M, C), 16),), dtype=torch.uint8, device=r.device)
+            p = L.ptr
+            a = L.BlockNormBwdArgs(p(dn), p(dr_out), r.data_ptr(), None if dn is None else w_pre.data_ptr(),
+                                   None if dn is None else rstd_pre.data_ptr(), p(y), p(w_post),
+                                   None if w_post is None else rstd_post.data_ptr(), p(gate), p(alpha), dr.data_ptr(),
+                                   p(dy), p(dgate), p(dw_pre), p(dw_post), p(dalpha), workspace.data_ptr(),
+                                   workspace.numel(), M, C, rcode, ycode)
+            L.check(L.load().samba_block_norm_bwd(ctypes.byref(a), L.stream_handle(stream)))
+    _lend(stream, *out.values())
     return out
 
 
