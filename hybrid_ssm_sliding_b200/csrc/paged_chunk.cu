@@ -111,9 +111,15 @@ __device__ __forceinline__ float chunk_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Maxima that keep a NaN: a row that sees one shows it.
 __device__ __forceinline__ float chunk_max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float chunk_max2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 // Whether the phase is over, asked ahead of a wait so that the answer is there by
@@ -162,9 +168,11 @@ __device__ __forceinline__ void umma_ss8_w(uint32_t d_tmem, uint64_t a_desc, uin
 // 2^x for a pair of arguments on the FMA pipe, to about 1e-4 (ample for
 // probabilities that are rounded next): x = j + f, j = rint(x) by adding 1.5 *
 // 2^23, 2^f a cubic fitted on [-1/2, 1/2] with value 1 at 0, j added to the
-// exponent.  Arguments below -125 give 2^-125, which no sum can notice.
+// exponent.  Arguments of -127 and less (hidden positions) give zero exactly: the
+// cubic's 1 less 127 in the exponent is a float's zero; above -127 the result may
+// be subnormal.  A NaN gives zero too, so the row's maximum has to carry it.
 __device__ __forceinline__ float2 chunk_ex2_poly(float2 v) {
-  const f2 x = pk2(fmaxf(v.x, -125.f), fmaxf(v.y, -125.f));
+  const f2 x = pk2(fmaxf(v.x, -127.f), fmaxf(v.y, -127.f));
   const f2 magic = pk2(12582912.f, 12582912.f);
   const f2 t = add2(x, magic);
   const f2 f = sub2(x, sub2(t, magic));
@@ -566,22 +574,23 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
           m4[i] = chunk_max3(sc[c], sc[c + 4], sc[c + 8]);
 #pragma unroll
           for (int j = 12; j < G - 4; j += 8) m4[i] = chunk_max3(m4[i], sc[c + j], sc[c + j + 4]);
-          m4[i] = fmaxf(m4[i], sc[c + G - 4]);
+          m4[i] = chunk_max2(m4[i], sc[c + G - 4]);
         }
-        const float mq = fmaxf(chunk_max3(m4[0], m4[1], m4[2]), m4[3]);
+        const float mq = chunk_max2(chunk_max3(m4[0], m4[1], m4[2]), m4[3]);
         if constexpr (KV8) {
           const float2 f = tile_sc[q * SPAN / 16];
-          m_tile = fmaxf(m_tile, fmaf(mq, factor_of(f), f.y));
+          m_tile = chunk_max2(m_tile, fmaf(mq, factor_of(f), f.y));
         } else {
-          m_tile = fmaxf(m_tile, mq * rowscale);
+          m_tile = chunk_max2(m_tile, mq * rowscale);
         }
       }
       if constexpr (KV8) read_done();
       float factor = 1.f;
       bool rescale = false;
-      if (m_tile > m_run + 8.f) {
+      if (!(m_tile <= m_run + 8.f)) {  // (or NaN)
         factor = chunk_ex2(m_run - m_tile);
-        m_run = m_tile;
+        // A score of NaN or infinity makes its row NaN from here on, as a softmax does.
+        m_run = chunk_max2(m_run, fmaf(m_tile, 0.f, m_tile));
         rescale = true;
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;

@@ -9,8 +9,8 @@ import torch
 from hybrid_ssm_sliding_b200 import _lib as L
 from hybrid_ssm_sliding_b200 import build as B
 from hybrid_ssm_sliding_b200 import ops
-from tests._paged import Case
-from tests.test_paged import check_attn, run_attn
+from tests._paged import Case, attend64
+from tests.test_paged import BF16_HALF, check_attn, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,57 @@ def test_wide_heads_where_scores_and_weights_share_columns(e4m3, window):
     o = run_attn(c, window)
     check_attn(c, window, o)
     assert all(torch.equal(run_attn(c, window), o) for _ in range(5))
+
+
+# ------------------------------------------------- what is not finite
+NEW = {"few rows": 3, "chunk": 150}
+
+
+def check_nonfinite(c, window, o):
+    """NaN where the definition in 64 bits has it, the usual bound elsewhere."""
+    want, mag = attend64(c, window)
+    o = o.cpu().double()
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    vsum = max(float(c.seq_values(b, "v").abs().sum(1).max()) for b in range(len(c.new)))
+    tol = BF16_HALF * want.abs() + ((2.0 ** -11 if c.e4m3 else BF16_HALF) + 2.0 ** -13) * mag
+    tol = tol + (2.0 ** -25 * vsum if c.e4m3 else 0)
+    assert float(((o - want).abs() - tol)[fine].max()) <= 0
+
+
+def poison_key(c, b, p, bad, head=0):
+    """Element 5 of the key at position p of sequence b."""
+    x = c.kc.float()
+    x[int(c.table[b, p // c.P]), head, p % c.P, 5] = bad
+    c.kc = x.to(c.kc.dtype)
+
+
+@pytest.mark.parametrize("which", NEW)
+@pytest.mark.parametrize("e4m3,d,bad", [(False, 64, "nan"), (False, 64, "inf"), (False, 128, "nan"),
+                                        (True, 64, "nan"), (True, 16, "nan"), (True, 128, "nan")])
+def test_a_visible_key_that_is_not_finite(e4m3, d, bad, which):
+    """At every position modulo 16: rows that see it become NaN, whichever kernel
+    takes them, and the others stay; a row that sees nothing else included."""
+    n = NEW[which]
+    for p in range(16):
+        c = Case([n, n], [0, 40], 4, 2, d, 16, e4m3, seed=100 + p)
+        c.q[c.start[0]:, :, 5] = 1.0                        # the score has the key's sign
+        poison_key(c, 0, p, float(bad))
+        poison_key(c, 1, 16 + p, float(bad), head=1)
+        check_nonfinite(c, 0, run_attn(c, 0))
+        check_nonfinite(c, 3, run_attn(c, 3))
+
+
+@pytest.mark.parametrize("which", NEW)
+def test_hidden_values_of_any_size_weigh_nothing(which):
+    """bf16 values of 2^127 at positions that some rows do not see: exactly nothing of them reaches those rows."""
+    n = NEW[which]
+    c = Case([n], [300], 4, 2, 64, 64, False, seed=140)
+    x = c.vc.float()
+    last = c.kv[0] - 1
+    x[int(c.table[0, last // 64]), :, last % 64] = 2.0 ** 127   # the last position: only the last row sees it
+    c.vc = x.to(torch.bfloat16)
+    for window in (0, 100):
+        o, (want, mag) = run_attn(c, window).cpu().double(), attend64(c, window)
+        tol = BF16_HALF * want.abs() + (BF16_HALF + 2.0 ** -13) * mag
+        assert float(((o - want).abs() - tol)[:n - 1].max()) <= 0
