@@ -663,12 +663,12 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
     const int64_t at = (int64_t)(t.seq_row0 + tok) * p.Hq + h;
     if (!SAMBA_CHECK(t.seq_row0 + tok < p.batch.rows && h < p.Hq && split < p.nsplit)) continue;
     if (p.npart == 1) {
-      p.o[at * HD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+      p.o[at * HD + d] = __float2bfloat16_rn(acc / L);  // (0 / 0 where every score was -infinity)
     } else {
       float* dst = p.ws + ((((int64_t)b * p.batch.max_q + tok) * p.Hq + h) * p.npart + split / p.cluster) * (HD + 2);
       dst[2 + d] = acc;
       if (d == 0) {
-        dst[0] = M;
+        dst[0] = L == L ? M : L;  // a split that saw NaN alone has no maximum
         dst[1] = L;
       }
     }
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   if (lane == 0) sl[warp] = L;
   __syncthreads();
   L = sl[0] + sl[1] + sl[2] + sl[3];
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const float inv = 1.f / L;  // (infinite where every score was -infinity: NaN)
   const int64_t at = (int64_t)s.row0 * p.Hq + i;
   if (!SAMBA_CHECK(s.row0 + i / p.Hq < p.batch.rows)) return;
   for (int d = threadIdx.x; d < HD; d += 128) {

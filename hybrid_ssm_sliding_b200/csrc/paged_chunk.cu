@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
       tc_fence_after();
       const bool store = live && SAMBA_CHECK(sq.row0 + tok < p.batch.rows && h < p.Hq && split < p.nsplit);
       float* part = p.ws + ((((int64_t)b * p.batch.max_q + tok) * p.Hq + h) * p.nsplit + split) * (HD + 2);
-      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      const float inv = 1.f / l_run;  // (infinite where every score was -infinity: NaN)
 #pragma unroll
       for (int q = 0; q < HD / 16; ++q) {
         uint32_t o[16];
