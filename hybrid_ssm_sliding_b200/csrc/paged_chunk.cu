@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
             amax = chunk_max3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
         }
         const int ex = min(max(log2i(amax), -60), 126) - 7;  // 2^7 <= amax 2^-ex < 2^8
-        const float by = exp2i(-ex);
+        // (e4m3 has no infinity: a row that holds one is NaN, which its softmax would be)
+        const float by = amax <= 3.402823466e38f ? exp2i(-ex) : __int_as_float(0x7fffffff);
         rowscale *= exp2i(ex);
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) {  // 16 elements

@@ -106,6 +106,18 @@ def test_a_whole_split_of_nan_keys(e4m3, which):
 
 
 @pytest.mark.parametrize("which", NEW)
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_a_query_that_is_not_finite(bad, e4m3, which):
+    """Its row and head become NaN, no other."""
+    n = NEW[which]
+    c = Case([n, 1], [70, 9], 4, 2, 64, 32, e4m3, seed=130)
+    c.q[c.start[0] + n - 2, 1, 7], c.q[c.start[1], 3, 0] = float(bad), float(bad)
+    check_nonfinite(c, 0, run_attn(c, 0))
+    check_nonfinite(c, 30, run_attn(c, 30))
+
+
+@pytest.mark.parametrize("which", NEW)
 def test_hidden_values_of_any_size_weigh_nothing(which):
     """bf16 values of 2^127 at positions that some rows do not see: exactly nothing of them reaches those rows."""
     n = NEW[which]
