@@ -36,9 +36,17 @@ __device__ __forceinline__ float exp2i(int k) { return __uint_as_float(static_ca
 __device__ __forceinline__ int log2i(float s) { return static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127; }
 
 // Scales are powers of two within these exponents.  The range is narrow enough
-// for one running maximum to serve scores and value scales together: a weight
-// that the attention loses below 2^-126 of it is below 2^-36 of the row's sum.
+// for one running maximum to serve scores s and value scales 2^e together: with
+// p' = 2^(s + e - m), m at least kScaledRef below the largest s + e, the sum of
+// p' 2^-e loses what lies below 2^-126, a part of under 2^-43 of it.
 constexpr int kScaleMin = -60, kScaleMax = 30;
+
+// The product with V takes p' rounded to f16, between 2^7 and 2^15 at a row's
+// largest s + e: full precision down to 2^-21 of that, nothing below 2^-32.  So a
+// page whose value scale is 2^20 times another's leaves the other's values (in
+// elements where its own codes are small) five bits at equal scores; with the
+// largest p' at 1 it left them none.
+constexpr float kScaledRef = 7.f;
 
 // The smallest k >= kScaleMin with amax <= 448 * 2^k (448 = 1.75 * 2^8), at
 // most kScaleMax, in whole-number arithmetic on the bits: no rounding decides it.

@@ -18,12 +18,13 @@
 // 8 columns, so nothing is spent on padding rows, and each thread
 // holds the scores of two query rows.  P^T then enters O^T = V^T P^T through one
 // in-register 8 x 8 transpose.  The running maximum moves only when a score exceeds
-// it by more than 2^8 (a warp vote; the result does not depend on the
-// reference), so the common case needs no reduction across lanes at all.
+// it by more than 2^8 (a warp vote), so the common case needs no reduction across
+// lanes at all.
 //
 // e4m3 codes become f16 in registers (exact), so the products run in f16:
-// queries are scaled by a power of two a row into [1, 2) first, and p' at
-// most 2^8 fits.  A bf16 cache multiplies in bf16.
+// queries are scaled by a power of two a row into [1, 2) first, and p' between 2^7
+// and 2^15 at a row's maximum fits and leaves f16's range to what lies below
+// (paged.cuh).  A bf16 cache multiplies in bf16.
 #include <algorithm>
 #include <cmath>
 
@@ -449,7 +450,9 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
         }
       }
     }
-    // move a row's reference maximum only when a score is past it by 2^8
+    // A row's reference lies kRef below its maximum and moves only when a score is
+    // past that maximum by 2^8.
+    constexpr float kRef = KV8 ? kScaledRef : 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float mx[2] = {-INFINITY, -INFINITY};
@@ -457,13 +460,13 @@ __global__ void __launch_bounds__(128) paged_split_kernel(const __grid_constant_
       for (int u = 0; u < NG; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e & 1] = fmaxf(mx[e & 1], s[nt][u][e]);
-      if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + 8.f || mx[1] > m[nt][1] + 8.f)) {
+      if (__any_sync(0xffffffffu, mx[0] > m[nt][0] + kRef + 8.f || mx[1] > m[nt][1] + kRef + 8.f)) {
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int x = 4; x <= 16; x <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], x));
-          const float mn = fmaxf(m[nt][e], mx[e]);
+          const float mn = fmaxf(m[nt][e], mx[e] - kRef);
           f[e] = m[nt][e] == mn ? 1.f : exp2_ap(m[nt][e] - mn);  // 0 while nothing was seen
           m[nt][e] = mn;
           l[nt][e] *= f[e];

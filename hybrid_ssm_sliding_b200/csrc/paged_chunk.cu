@@ -586,12 +586,15 @@ __global__ void __launch_bounds__(ChunkCfg<HD, KV8>::THREADS, ChunkCfg<HD, KV8>:
         }
       }
       if constexpr (KV8) read_done();
+      // the row's reference m_run lies kRef below its maximum
+      constexpr float kRef = KV8 ? kScaledRef : 0.f;
       float factor = 1.f;
       bool rescale = false;
-      if (!(m_tile <= m_run + 8.f)) {  // (or NaN)
-        factor = chunk_ex2(m_run - m_tile);
+      if (!(m_tile <= m_run + kRef + 8.f)) {  // (or NaN)
         // A score of NaN or infinity makes its row NaN from here on, as a softmax does.
-        m_run = chunk_max2(m_run, fmaf(m_tile, 0.f, m_tile));
+        const float m_new = chunk_max2(m_run, fmaf(m_tile, 0.f, m_tile) - kRef);
+        factor = chunk_ex2(m_run - m_new);
+        m_run = m_new;
         rescale = true;
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;

@@ -130,3 +130,49 @@ def test_hidden_values_of_any_size_weigh_nothing(which):
         o, (want, mag) = run_attn(c, window).cpu().double(), attend64(c, window)
         tol = BF16_HALF * want.abs() + (BF16_HALF + 2.0 ** -13) * mag
         assert float(((o - want).abs() - tol)[:n - 1].max()) <= 0
+
+
+# ------------------------------------------------- weights far below the largest
+def lost_weights(c, window):
+    """What f16 weights may lose of each output, in 64 bits: a weight times its value's scale is held relative to a
+    row's largest at 2^7 or more, so each is off by at most half of f16's smallest step, 2^-25 there (what it
+    loses above is half a step of itself, and counted with the sum of p |v|)."""
+    tol = torch.zeros((c.T, c.Hq, c.d), dtype=torch.float64)
+    grp = c.Hq // c.Hkv
+    for b, n in enumerate(c.new):
+        k, v = c.seq_values(b, "k"), c.seq_values(b, "v")
+        page = c.table[b, torch.arange(c.kv[b]) // c.P].long()
+        vs = c.vs.double()[page].T.repeat_interleave(grp, 0)[:, None, :]                     # [Hq, 1, kv]
+        q = c.q[c.start[b]:c.start[b + 1]].double().transpose(0, 1)
+        key, pos = torch.arange(c.kv[b]), torch.arange(c.past[b], c.kv[b])
+        see = key[None] <= pos[:, None]
+        if window:
+            see &= key[None] + window > pos[:, None]
+        s = torch.einsum("hnd,hkd->hnk", q, k.repeat_interleave(grp, 0)) * c.d ** -0.5
+        w = torch.where(see, torch.exp(s) * vs, torch.zeros((), dtype=torch.float64))
+        w = w / w.amax(-1, keepdim=True) * 2.0 ** 7
+        codes = v.abs().repeat_interleave(grp, 0) / vs.transpose(1, 2)
+        lost = 2.0 ** -25 * see.double() @ codes / (w / vs).sum(-1, keepdim=True)
+        tol[c.start[b]:c.start[b + 1]] = lost.transpose(0, 1)
+    return tol
+
+
+@pytest.mark.parametrize("which", NEW)
+@pytest.mark.parametrize("apart", [10, 20, 26, 40])
+def test_small_scales_beside_a_large_one(apart, which):
+    """A page of a value scale 2^apart times the others', zero in half of its
+    elements: there the others' values are the answer."""
+    n = NEW[which]
+    c = Case([n, n], [79, 700], 8, 2, 64, 16, True, seed=150 + apart)
+    c.vs = c.vs * 2.0 ** -16                                # all within 2^-60 .. 2^30
+    for b in range(2):
+        pg = int(c.table[b, 1])
+        c.vs[pg] = c.vs[pg] * 2.0 ** apart
+        x = c.vc.float()
+        x[pg, :, :, ::2] = 0
+        c.vc = x.to(torch.float8_e4m3fn)
+    for window in (0, 0 if n == 150 else 75):
+        o = run_attn(c, window).cpu().double()
+        want, mag = attend64(c, window)
+        tol = BF16_HALF * want.abs() + (2.0 ** -11 + 2.0 ** -13) * mag + lost_weights(c, window)
+        assert float(((o - want).abs() / tol).max()) <= 1
