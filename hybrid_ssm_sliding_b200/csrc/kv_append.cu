@@ -118,7 +118,8 @@ __device__ __forceinline__ float finite_abs(float x) {  // |x|, 0 for NaN and in
 template <bool KV8>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(128) float table[];  // [rows][rot / 2] cosines, then sines; a slice's queries
-  __shared__ int span[3];                          // q_start[b], q_start[b + 1], kv_len[b]
+  __shared__ __align__(16) int found[kAppendThreads / 32];  // the item's sequence, if the warp came upon it
+  __shared__ SeqSpan spans[kAppendThreads / 32];
   __shared__ uint64_t landed;                      // the slice's copies
   __shared__ float warp_max[kAppendThreads / 32];
   __shared__ int abort_flag;
@@ -135,27 +136,29 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
   }
   pdl_launch_dependents();
   pdl_wait();
-  // the sequence: the last one whose first item number is at most this one
-  const int B = (int)a.batch.batch;
-  int b = -1;
-  for (int i0 = 0; i0 < B; i0 += kAppendThreads) {
-    const int i = i0 + tid;
-    int q0 = 0, q1 = 0, kv = 0;
-    if (i < B) q0 = a.batch.q_start[i], q1 = a.batch.q_start[i + 1], kv = a.batch.kv_len[i];
-    b += __syncthreads_count(i < B && static_cast<int64_t>(q0 / P) + 2 * i <= item);
-    if (i == b) span[0] = q0, span[1] = q1, span[2] = kv;
-    if (blockIdx.x == 0 && i < B) check_span(a.batch, P, q0, q1, kv, true);  // one block reports what is out of range
+  // The sequence that has this item among its numbers: one at most where the
+  // sequences are in order, and one that is out of range has none.
+  int b = -1, w = 0;
+  SeqSpan s{0, 0, 0};
+  for (int i = tid; i < (int)a.batch.batch; i += kAppendThreads) {
+    const SeqSpan t = seq_span(a.batch, P, i, blockIdx.x == 0);  // one block reports what is out of range
+    const int64_t at = item - (t.row0 / P + 2 * static_cast<int64_t>(i));
+    if (t.n > 0 && at >= 0 && at <= ((t.kv - 1) >> pshift) - ((t.kv - t.n) >> pshift)) b = i, s = t;
   }
-  if (b < 0) return;
+  const int top = __reduce_max_sync(0xffffffffu, b);
+  if (b == top && (b >= 0 || lane == 0)) found[warp] = top, spans[warp] = s;
   __syncthreads();
-  const int j = item - span[0] / P - 2 * b;  // page of the sequence's new rows
-  const SeqSpan s = check_span(a.batch, P, span[0], span[1], span[2], false);
-  if (s.n == 0) return;
+  b = -1;
+#pragma unroll
+  for (int k = 0; k < kAppendThreads / 32; ++k)
+    if (found[k] > b) b = found[k], w = k;
+  if (b < 0) return;
+  s = spans[w];
+  const int j = item - s.row0 / P - 2 * b;       // page of the sequence's new rows
   const int first = s.kv - s.n;                  // position of the sequence's first new row
   const int col = (first >> pshift) + j;         // block_table column
   const int lo = j == 0 ? first : col << pshift; // positions [lo, hi) of this item
   const int hi = min(s.kv, (col + 1) << pshift);
-  if (j < 0 || hi <= lo) return;
   const bool keys = part < p.nkv;                // this block's part: keys and values, or queries
   const int row_lo = keys ? 0 : (part - p.nkv) / p.nhead * p.qrows;
   const int n = keys ? hi - lo : min(hi - lo - row_lo, p.qrows);  // its rows of the item, from row_lo

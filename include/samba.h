@@ -580,9 +580,11 @@ int samba_swa_step_noalloc(const void* q_t, const void* k_t, const void* v_t, vo
  * The kernels check what they read: rows [q_start[b], q_start[b+1]) within
  * [0, rows), n_b <= max_q, n_b <= kv_len[b] <= max_kv, kv_len[b] <= max_pages *
  * page_size, and every page number used within [0, num_pages).  A sequence
- * that fails is skipped (its rows are not written); a page that fails takes no
- * keys and values and reads as zeros; SAMBA_ERR_BATCH is recorded in the status
- * word (with max_q 0 no kernel runs, and none checks).
+ * that fails is skipped (its rows are not written) and the others are not
+ * touched by that; a page that fails takes no keys and values and reads as
+ * zeros; SAMBA_ERR_BATCH is recorded in the status word (with max_q 0 no kernel
+ * runs, and none checks).  Of two sequences that pass, but the later one's rows
+ * come before the earlier one's, samba_kv_append may skip either.
  * Limits: page_size 16, 32, 64, 128 or 256; d 16, 32, 64 or 128; num_pages *
  * Hkv < 2^31; rows and max_kv < 2^30; batch <= 65535; Hkv <= 65535.
  */

@@ -10,7 +10,7 @@ from hybrid_ssm_sliding_b200 import _lib as L
 from hybrid_ssm_sliding_b200 import build as B
 from hybrid_ssm_sliding_b200 import ops
 from tests._paged import Case, attend64
-from tests.test_paged import BF16_HALF, check_attn, run_attn
+from tests.test_paged import BF16_HALF, check_attn, make_freqs, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -176,3 +176,42 @@ def test_small_scales_beside_a_large_one(apart, which):
         want, mag = attend64(c, window)
         tol = BF16_HALF * want.abs() + (2.0 ** -11 + 2.0 ** -13) * mag + lost_weights(c, window)
         assert float(((o - want).abs() / tol).max()) <= 1
+
+
+# ------------------------------------------------- batches out of order
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("value", [999, -5, -2 ** 31, 2 ** 31 - 1, 0, 40])
+@pytest.mark.parametrize("B", [5, 300])
+def test_an_entry_of_q_start_out_of_range_costs_its_neighbours_only(B, value, e4m3):
+    """The sequences on both sides of the entry fail; every other one gets its keys, values and
+    rotated queries, as from a batch without the fault, and attends them."""
+    new = [(3, 1, 17, 2, 0)[b % 5] for b in range(B)]
+    bad = B // 2                                                   # the entry between sequences bad - 1 and bad
+    c = Case(new, [(b * 7) % 40 for b in range(B)], 4, 2, 32, 16, e4m3, seed=160 + B)
+    fr, q, k, v = make_freqs(32).cuda(), c.q.cuda(), c.k.cuda(), c.v.cuda()
+    res = []
+    for broken in (False, True):
+        cache, batch = c.gpu()
+        if broken:
+            batch.q_start[bad] = value
+        before = cache.k.view(torch.uint8).clone()
+        qo, o = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+        ops.kv_append(q, k, v, cache, batch, freqs=fr, q_out=qo)
+        assert ops.get_status() == (L.SAMBA_ERR_BATCH if broken else L.SAMBA_OK)
+        ops.paged_attn(qo, cache, batch, o=o)
+        assert ops.get_status() == (L.SAMBA_ERR_BATCH if broken else L.SAMBA_OK)
+        pools = [t.view(torch.uint8).clone() if t.dtype != torch.float32 else t.clone()
+                 for t in (cache.k, cache.v, cache.k_scale, cache.v_scale) if t is not None]
+        res.append((qo, o, pools))
+    (q0, o0, p0), (q1, o1, p1) = res
+    start = [*c.start[:bad], value, *c.start[bad + 1:]]
+    for b in range(B):
+        rows = slice(c.start[b], c.start[b + 1])
+        pages = c.table[b, :-(-c.kv[b] // c.P)].long().cuda()
+        if b in (bad - 1, bad):
+            assert start[b] < 0 or not 0 <= start[b + 1] - start[b] <= c.max_q     # out of range
+            assert bool((q1[rows] == 7).all()) and bool((o1[rows] == 7).all())
+            assert torch.equal(p1[0][pages], before[pages])
+        else:
+            assert torch.equal(q0[rows], q1[rows]) and torch.equal(o0[rows], o1[rows]), b
+            assert all(torch.equal(x[pages], y[pages]) for x, y in zip(p0, p1)), b
