@@ -61,6 +61,27 @@ __device__ __forceinline__ f2 sigmoid2(f2 v) {
   return pk2(sigmoidf(t.x), sigmoidf(t.y));
 }
 
+// The backward pass needs s = sigmoid(x) and 1 - s, each to a part of itself (1 less
+// s has no digits left where s is near 1): with E = exp(-x) they are 1 / (1 + E) and E
+// times that.  E is what is kept between the two places that use s; it stops
+// short of infinity, where s is 0, and keeps a NaN.
+__device__ __forceinline__ f2 exp_neg2(f2 x) {
+  const float2 a = up2(mul2(x, both(-1.44269504f)));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.x) : "f"(3.402823466e38f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.y) : "f"(3.402823466e38f));
+  return pk2(e.x, e.y);
+}
+__device__ __forceinline__ f2 one_over_one_plus2(f2 e) {
+  const float2 d = up2(add2(e, both(1.f)));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return pk2(r.x, r.y);
+}
+
 // How a call is cut up: rows a group, threads a row (a multiple of 32), and
 // where a tensor lies in a stage.
 struct NormShape {
@@ -389,9 +410,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
         if (has_y) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            z[i] = has_g ? sigmoid2(z[i]) : both(1.f);
+            z[i] = has_g ? exp_neg2(z[i]) : both(0.f);
             yh[i] = mul2(yh[i], rsy2);
-            const f2 ci = mul2(mul2(c[i], z[i]), yh[i]);
+            const f2 ci = mul2(mul2(c[i], has_g ? one_over_one_plus2(z[i]) : both(1.f)), yh[i]);
             q1 = fma2(ci, g[i], q1);
             q2 = fma2(ci, x[i], q2);
           }
@@ -412,9 +433,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_bwd_kernel(const __grid_const
           f2 dz[4], dy[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f2 gs = mul2(g[i], z[i]), dt = mul2(gs, c[i]);
+            const f2 sg = has_g ? one_over_one_plus2(z[i]) : both(1.f);
+            const f2 gs = mul2(g[i], sg), dt = mul2(gs, c[i]);
             a_post[i] = fma2(gs, yh[i], a_post[i]);
-            dz[i] = mul2(mul2(dt, yh[i]), sub2(both(1.f), z[i]));
+            dz[i] = mul2(mul2(dt, yh[i]), mul2(z[i], sg));
             dy[i] = fma2(rsy2, dt, mul2(both(-m2), yh[i]));
           }
 #pragma unroll
