@@ -3,7 +3,8 @@
 //
 // The rotation turns pairs of elements by position * frequency.  The turn is
 // reduced modulo one in fp64 (a position of 10^6 leaves fp32 with no digits
-// of the angle), its sine and cosine are fp32.  An 8-bit cache holds e4m3
+// of the angle), its sine and cosine are fp32, with what the turn loses in fp32
+// put back to first order (without, the angle's error of 1e-7 is a key's largest).  An 8-bit cache holds e4m3
 // codes with one power-of-two scale s a (page, kv head): the smallest with
 // max |x| <= 448 s, so a block's largest value keeps the full three bits and
 // growing a scale only shifts the codes stored before.
@@ -173,7 +174,12 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
       for (int r = warp; r < n; r += kAppendThreads / 32) {
         double turn = static_cast<double>(lo + row_lo + r) * f;
         turn -= rint(turn);
-        sincospif(2.f * static_cast<float>(turn), si + r * half + c, co + r * half + c);
+        const float near = static_cast<float>(turn);
+        float sn, cs;
+        sincospif(2.f * near, &sn, &cs);
+        const float rest = 6.28318531f * static_cast<float>(turn - near);  // the angle that rounding the turn lost
+        si[r * half + c] = fmaf(rest, cs, sn);
+        co[r * half + c] = fmaf(-rest, sn, cs);
       }
     }
     __syncthreads();

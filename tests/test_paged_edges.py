@@ -3,13 +3,15 @@ row tiles that end inside a warp, products that share tensor memory, values
 that are not finite, weights far below the largest, batches out of order.
 Tolerances as in test_paged.py; what a test adds to them stands at the test."""
 
+import math
+
 import pytest
 import torch
 
 from hybrid_ssm_sliding_b200 import _lib as L
 from hybrid_ssm_sliding_b200 import build as B
 from hybrid_ssm_sliding_b200 import ops
-from tests._paged import Case, attend64
+from tests._paged import Case, attend64, rotated64
 from tests.test_paged import BF16_HALF, check_attn, make_freqs, run_attn
 
 pytestmark = pytest.mark.gpu
@@ -215,3 +217,28 @@ def test_an_entry_of_q_start_out_of_range_costs_its_neighbours_only(B, value, e4
         else:
             assert torch.equal(q0[rows], q1[rows]) and torch.equal(o0[rows], o1[rows]), b
             assert all(torch.equal(x[pages], y[pages]) for x, y in zip(p0, p1)), b
+
+
+# ------------------------------------------------- angles
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_next_to_quarter_turns(inter):
+    """Angles within 2^-22 turns a position of quarter turns, one element of each pair zero: what is left is x times
+    a sine or cosine down to 2^-20, held to a part of itself.  The sine and cosine
+    are off by 2^-23 of themselves, their turn's rest adds one rounding and the
+    product one (2^-24 each), then the result is rounded once."""
+    n, d = 97, 64
+    c = Case([n], [0], 2, 2, d, 32, False, seed=170)
+    j = torch.arange(d // 2, dtype=torch.float64)
+    turns = 0.25 + 2.0 ** -22 * (1 + 0.137 * j) * torch.where(j.long() % 2 == 0, 1.0, -1.0)
+    freqs = turns * 2 * math.pi
+    hi = slice(1, d, 2) if inter else slice(d // 2, d)
+    c.q[..., hi], c.k[..., hi] = 0, 0
+    cache, batch = c.gpu()
+    q = ops.kv_append(c.q.cuda(), c.k.cuda(), c.v.cuda(), cache, batch, freqs=freqs.cuda(), interleaved=inter)
+    rows = torch.cat([cache.k[int(pg)].transpose(0, 1) for pg in c.table[0, :4]])[:n]
+    for x, got in ((c.q, q), (c.k, rows)):
+        want = rotated64(x, torch.arange(n), freqs, inter)
+        # position * angle in 64 bits carries 2^-52 of up to 152 radians itself: 2^-44
+        tol = (BF16_HALF + 2.0 ** -22) * want.abs() + 2.0 ** -44 * x.double().abs().amax(-1, keepdim=True)
+        assert float(((got.cpu().double() - want).abs() - tol).max()) <= 0
+    assert ops.get_status() == L.SAMBA_OK
