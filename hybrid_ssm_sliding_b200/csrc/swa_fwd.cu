@@ -468,6 +468,8 @@ __global__ void __launch_bounds__(352, 1)
         if (jt > 0) {
           if (!wait(bar_o, (t - 1) & 1)) { ok = false; break; }
           tc_fence_after();
+        } else {
+          __syncwarp();  // (as the vote in the wait: the stores below are the whole warp's)
         }
         // p = 2^(s·scale·log2e - m) in packed pairs; every SWA_POLY-th pair on
         // the FMA pipe, the rest on MUFU; four partial sums; each 16 packed
@@ -496,7 +498,9 @@ __global__ void __launch_bounds__(352, 1)
         }
         const float2 r01 = up2(add2(add2(acc4[0], acc4[1]), add2(acc4[2], acc4[3])));
         l_run = l_run * factor + (r01.x + r01.y);
-        if (jt > 0 && rescale) {
+        // Loads and stores of tensor memory are the whole warp's, so the warp rescales
+        // if one row does; factor is 1 in the rows that keep their maximum.
+        if (__any_sync(0xffffffffu, jt > 0 && rescale)) {
           uint32_t o[16];
 #pragma unroll
           for (int q = 0; q < HD / 16; ++q) {
