@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += 32) {
         uint32_t r[32];
+        __syncwarp();              // lanes without a row or column left the last step early
         tmem_ld32(t_row + c0, r);  // warp-collective: every lane, whatever its row
         tc_wait_ld();
         if (row >= p.M || !SAMBA_CHECK(row >= 0 && n0 + c0 < p.N)) continue;

@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, GROUP>::THREADS, 1)
           ok = wait(&bars[BB_O], (m - 1) & 1);
           if (!ok) break;
           tc_fence_after();
+        } else {
+          __syncwarp();  // (as the vote in the wait: the stores below are the whole warp's)
         }
         tmem_st16(tmem + lane_off + Cfg::COL_P + 16 * cc, pk);
         tmem_st16(tmem + lane_off + Cfg::COL_DS + 16 * cc, dk);
@@ -394,6 +396,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, GROUP>::THREADS, 1)
           if (q % Cfg::NCW != part) continue;  // the parts of a quarter share the columns
           uint32_t t16[16];
           if (nq > 0) {
+            __syncwarp();  // the load is the whole warp's, the stores of the last step are not
             tmem_ld16(tmem + lane_off + col + 16 * q, t16);
             tc_wait_ld();
           } else {
@@ -623,6 +626,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, GROUP>::THREADS, 1)
           ok = wait(&bars[BB_O], (t - 1) & 1);
           if (!ok) break;
           tc_fence_after();
+        } else {
+          __syncwarp();  // (as the vote in the wait: the stores below are the whole warp's)
         }
         tmem_st16(tmem + lane_off + Cfg::COL_DS + 16 * cc, dk);
       }
@@ -641,6 +646,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, GROUP>::THREADS, 1)
       for (int q = 0; q < HD / 16; ++q) {
         if (q % Cfg::NCW != part) continue;  // the parts of a quarter share the columns
         uint32_t t16[16];
+        __syncwarp();  // the load is the whole warp's, the stores of the last step are not
         tmem_ld16(tmem + lane_off + Cfg::COL_DQ + 16 * q, t16);
         tc_wait_ld();
         if (irow >= p.L || !SAMBA_CHECK(irow >= 0 && b < p.B && g * GROUP + hh < p.Hq)) continue;
