@@ -650,7 +650,16 @@ int samba_kv_append(const samba_kv_append_args* args, samba_stream_t stream);
  * block_table entries may hold anything.  What the cache holds beyond
  * kv_len is not read as a value (it may be NaN).  Where a call has several
  * rows of a sequence, a NaN or an infinity in a value that one of them sees
- * may reach the others (as 0 * NaN); masked keys never matter.
+ * may reach the others (as 0 * NaN); masked keys never matter.  A row that sees a
+ * score of NaN or +infinity, or none above -infinity, is NaN, as its softmax is.
+ * Scores, maxima and sums are fp32; the weights are rounded for the product with
+ * V, to bf16, or with SAMBA_E4M3 to f16 on a scale where the row's largest weight
+ * times value scale is 2^7 or more: 11 bits down to 2^-21 of it, nothing below 2^-32.
+ * Calls of more than 64 rows a kv head (max_q * Hq / Hkv) over an e4m3 cache
+ * take a query row as two e4m3 numbers an element, bf16's eight bits down to 2^-10
+ * of the row's largest element and 2^-18 of that below.  The bounds choose the
+ * kernel of the whole call: single tokens beside a long chunk take as long as
+ * chunks, so they are better off in a call of their own.
  *   q, o  [rows, Hq, d] bf16; scale <= 0 selects 1/sqrt(d)
  * Limits: Hq / Hkv <= 16, max_q * Hq < 2^30, window < 2^30.  The workspace is caller-owned
  * device memory of samba_paged_attn_workspace_size() bytes, 16-byte aligned,
