@@ -726,7 +726,15 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
 
 // ------------------------------------------------------------------ launcher
 // Query rows a kv head up to which a call goes through the split kernel here:
-// its tiles of 16 rows each read the keys again.
+// its tiles of 16 rows each read the keys again, so its time grows with the rows, and
+// paged_chunk.cu's does not up to 128.  us here and there, 32 heads over 4 of 64:
+//   rows                  32           64           96
+//   1 x 8192, 8 bits      15.0 17.1    16.8 18.6    18.4 19.9
+//   16 x 2048, 8 bits     17.8 24.6    25.7 28.0    43.2 31.7
+//   16 x 2048, bf16       18.0 23.3    36.1 26.4    51.4 28.6
+//   16 x 16384, 8 bits    63.7 101     131 105      190 109
+//   64 x 4096, bf16       115 113      205 115      298 115
+// 64 is the last multiple of 32 where some of these gain, not where all do.
 constexpr int64_t kFewRows = 64;
 
 // Splits of a row tile's positions: as many as the SMs hold at once (64

@@ -56,8 +56,10 @@ def _ops():
     n = lambda *s: torch.randn(s, generator=torch.Generator(device="cuda").manual_seed(7), device="cuda")  # noqa: E731
     r, y, w, al = n(T, DM), n(T, DM).bfloat16(), n(DM), n(DM) + 1
 
+    pool, batch = c.gpu()
+
     def run(stream=None):
-        cache, batch = c.gpu()
+        cache = ops.PagedKv(*[t.clone() for t in (pool.k, pool.v, pool.k_scale, pool.v_scale)])
         rs, rsy = torch.empty((T,), device="cuda"), torch.empty((T,), device="cuda")
         if stream is not None:
             stream.wait_stream(torch.cuda.current_stream())
@@ -65,8 +67,8 @@ def _ops():
         o = ops.paged_attn(qr, cache, batch, stream=stream)
         r1, n1 = ops.block_norm_fwd(r, w, y=y, w_post=w, gate=y, alpha=al, rstd_pre=rs, rstd_post=rsy, stream=stream)
         g = ops.block_norm_bwd(n1, r1, w, rs, dr_out=r1, y=y, w_post=w, rstd_post=rsy, gate=y, alpha=al, stream=stream)
-        return (qr, o, cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale, batch.q_start,
-                batch.kv_len, batch.block_table, r1, n1, rs, rsy, *g.values())  # (the inputs too: the caller keeps them)
+        return (qr, o, cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale, r1, n1, rs, rsy,
+                *g.values())  # (the inputs too: the caller keeps them)
     return run
 
 
@@ -123,3 +125,23 @@ def test_outputs_freed_by_the_caller_are_not_reused_under_it(make):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(read, want))
     del held
+
+
+@pytest.mark.parametrize("make", [_stack, _ops], ids=["stack", "ops"])
+def test_a_call_on_a_stream_that_joins_a_capture(make):
+    """Captured on one stream, called on another that was forked from it."""
+    run = make()
+    want = [t.clone() for t in run()]
+    first, side = torch.cuda.Stream(), torch.cuda.Stream()
+    run(side)                               # what a first call loads is loaded
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(first), torch.cuda.graph(graph, stream=first):
+        got = run(side)
+        first.wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ops.get_status() == L.SAMBA_OK
+    same = [torch.equal(a, b) for a, b in zip(got, want)]
+    assert all(same), same
